@@ -79,7 +79,11 @@ typedef int32_t vs_dtype;
 #define VS_ROW_DUP_SUPPORT_ID (1u << 3)        /* a recorded id repeated: counted once */
 #define VS_ROW_NONFINITE_INPUT (1u << 4)       /* NaN/inf logit: outputs NaN, valid 0 */
 #define VS_ROW_DEVICE_TIMEOUT (1u << 5)        /* a bounded device wait gave up: outputs unreliable */
-#define VS_ROW_EMPTY_SUPPORT (1u << 6)         /* vs_support_lmhead_score: no kept id, lp_S NaN */
+#define VS_ROW_EMPTY_SUPPORT (1u << 6)         /* vs_support_lmhead_score: no kept id, lp_S NaN;
+                                                  vs_sample, vs_topk_logprob: every token masked;
+                                                  vs_distill_*: no listed id (or no teacher mass) */
+#define VS_ROW_BAD_PARAM (1u << 7)             /* vs_sample, vs_topk_logprob, vs_distill_*: a per-row
+                                                  setting outside its range */
 
 /* bytes of saved state per row written when VS_WANT_GRAD is set */
 #define VS_CTX_BYTES_PER_ROW 64
@@ -439,6 +443,134 @@ vs_status vs_support_lmhead_score(int32_t rows, int32_t vocab, int32_t hidden_di
                                   int32_t support_width, int64_t support_ld, uint32_t flags,
                                   const vs_score_out* out, float* support_logits,
                                   int64_t logits_ld, void* stream);
+
+/* Largest vocabulary of vs_sample, vs_topk_logprob and vs_distill_*. */
+#define VS_MAX_ROW_VOCAB (1 << 20)
+/* Largest k of vs_topk_logprob. */
+#define VS_MAX_TOPK 1024
+
+/* Arguments of vs_sample.  Per-row arrays or, where NULL, one scalar for all
+ * rows; the filters as in vs_score_args (disabled by top_k <= 0 or >= vocab,
+ * top_p >= 1, min_p <= 0). */
+typedef struct vs_sample_args {
+  int32_t rows;  /* R >= 0 */
+  int32_t vocab; /* 1 .. VS_MAX_ROW_VOCAB */
+  int64_t ld;    /* row stride of logits, in elements, >= vocab */
+  vs_dtype dtype;
+  const void* logits;       /* [R, ld]; -inf marks a masked token */
+  const float* temperature; /* [R], 0 = greedy (the first token of the order) */
+  float temperature_scalar; /* finite, >= 0 */
+  const int32_t* top_k;
+  int32_t top_k_scalar;
+  const float* top_p;
+  float top_p_scalar; /* in (0, 1] */
+  const float* min_p;
+  float min_p_scalar;   /* in [0, 1) */
+  const float* uniform; /* [R] the row's random number, in [0, 1] */
+} vs_sample_args;
+
+/* One token per row from a given uniform number ([xorl] section 3: the
+ * transform program of vs_score_fwd, temperature then stable token-id top-k
+ * then inclusive top-p then min-p relative to the row max; the caller's number
+ * in the place of the program's seeded noise).  With w_j = exp((l_j - max l) /
+ * T), the row in the total order (logit descending, token id ascending) and
+ * C_i the running sum of w:
+ *   n_k = min(top_k, unmasked tokens), n_p = first i with C_i >= top_p C_{n_k},
+ *   n_m = number of tokens with w >= min_p, n = min(n_k, n_p, n_m);
+ *   token[r] = the first i <= n with C_i > u C_n (u = 1: the n-th),
+ *   logprob[r] = log(w_token / C_n), support_size[r] = n.
+ * Sums are exact (fixed point, w in fp64), so equal inputs give equal tokens
+ * on every call and every batch.  A logit of -inf is a masked token: it is in
+ * no set, whatever the filters.  Rows without a token get -1, NaN and 0: every
+ * token masked (VS_ROW_EMPTY_SUPPORT), a NaN or +inf logit
+ * (VS_ROW_NONFINITE_INPUT), or a setting outside its range: T negative or not
+ * finite, top_p <= 0, min_p > 1, u outside [0, 1], or NaN (VS_ROW_BAD_PARAM).
+ * logprob, support_size and status may be NULL.  No workspace.
+ * VS_ERR_INVALID_ARG as for vs_score_fwd; VS_ERR_UNSUPPORTED for a vocab
+ * above VS_MAX_ROW_VOCAB. */
+vs_status vs_sample(const vs_sample_args* args, int32_t* token, float* logprob,
+                    int32_t* support_size, uint32_t* status, void* stream);
+
+/* The first k tokens of each row in the total order (logit descending, token
+ * id ascending) and their log-probabilities over the whole row,
+ *   logprob[r, i] = l / T - log sum_j exp(l_j / T):
+ * a teacher's list for vs_distill_fwd from logits in memory
+ * (vs_fused_lmhead_score gives the same two outputs from hidden states).
+ * ids and logprob are [rows, out_ld], the first k of each row written; -1 and
+ * -inf where the row has fewer than k unmasked (not -inf) tokens.  Rows with a
+ * NaN or +inf logit, or a temperature that is not positive and finite: -1 and
+ * NaN (status as for vs_sample).  1 <= k <= min(vocab, VS_MAX_TOPK);
+ * VS_ERR_UNSUPPORTED beyond VS_MAX_TOPK or VS_MAX_ROW_VOCAB.  logprob and
+ * status may be NULL.  No workspace. */
+vs_status vs_topk_logprob(int32_t rows, int32_t vocab, int64_t ld, vs_dtype dtype,
+                          const void* logits, const float* temperature, float temperature_scalar,
+                          int32_t k, int32_t* ids, float* logprob, int64_t out_ld,
+                          uint32_t* status, void* stream);
+
+/* Arguments shared by vs_distill_fwd and vs_distill_bwd. */
+typedef struct vs_distill_args {
+  int32_t rows;  /* R >= 0 */
+  int32_t vocab; /* 1 .. VS_MAX_ROW_VOCAB */
+  int64_t ld;    /* row stride of logits, in elements, >= vocab */
+  vs_dtype dtype;
+  const void* logits;       /* [R, ld] the student's */
+  const float* temperature; /* [R] (> 0, finite), or NULL to use temperature_scalar */
+  float temperature_scalar;
+  /* the teacher's list: [R, teacher_ld], the first teacher_width of each row
+   * used; -1 = padding anywhere in the row */
+  const int32_t* teacher_ids;
+  const float* teacher_logprob;
+  int32_t teacher_width; /* 0 .. VS_MAX_SUPPORT_WIDTH */
+  int64_t teacher_ld;    /* >= teacher_width */
+  int32_t tail;          /* 0: list mode, 1: tail mode (below) */
+} vs_distill_args;
+
+/* Outputs of vs_distill_fwd; every pointer may be NULL. */
+typedef struct vs_distill_out {
+  float* loss;      /* [R] */
+  uint8_t* valid;   /* [R] 1 iff the row has a listed id (with teacher mass) and is finite */
+  uint32_t* status; /* [R] VS_ROW_* bits */
+  void* ctx;        /* [R, VS_CTX_BYTES_PER_ROW] saved state for vs_distill_bwd, 16-byte aligned */
+  /* the gradient in the same call, when the rows' upstream gradients are
+   * known beforehand: dlogits [R, grad_ld] (dl_dtype, as in vs_score_bwd)
+   * is overwritten with g_loss[r] dloss_r / dl (g_loss NULL = 1) */
+  const float* g_loss;
+  void* dlogits;
+  vs_dtype dl_dtype;
+  int64_t grad_ld;
+} vs_distill_out;
+
+/* Distillation from a teacher's top log-probabilities (lists as vs_topk_logprob
+ * and vs_fused_lmhead_score write them).  Per row, with L its kept list (ids
+ * in [0, vocab), the first occurrence of each), q = softmax(l / T) over the
+ * vocabulary, lp the teacher's values:
+ *   list mode: a = softmax(lp) over L (lp may be any logits),
+ *     loss = sum_L a_k (log a_k - log q_k);
+ *   tail mode: a_k = exp(lp_k), a_t = max(0, 1 - sum a), q_t = the sum of q
+ *     outside L,  loss = sum_L a_k (log a_k - log q_k) + a_t (log a_t - log q_t).
+ * Terms with no teacher mass are 0; the tail term is 0 when no unmasked token
+ * lies outside L.  A logit of -inf is a masked token (q = 0; loss +inf when
+ * the teacher gives it mass).  Rows without a listed id (or, in list mode,
+ * without teacher mass): loss 0, valid 0, VS_ROW_EMPTY_SUPPORT.  Rows with a
+ * NaN or +inf logit, only masked ones, or a listed lp of NaN or +inf
+ * (VS_ROW_NONFINITE_INPUT), or a bad temperature (VS_ROW_BAD_PARAM): loss NaN,
+ * valid 0.  Both kinds have a zero gradient.  Ids outside the range set
+ * VS_ROW_BAD_SUPPORT_ID and are skipped, repeats VS_ROW_DUP_SUPPORT_ID.
+ * No workspace; sums in fixed order.  VS_ERR_INVALID_ARG as for vs_score_fwd
+ * and when dlogits overlaps logits; VS_ERR_UNSUPPORTED for a teacher_width
+ * above VS_MAX_SUPPORT_WIDTH or a vocab above VS_MAX_ROW_VOCAB. */
+vs_status vs_distill_fwd(const vs_distill_args* args, const vs_distill_out* out, void* stream);
+
+/* Gradient of the per-row losses, from the forward's saved state:
+ *   dl_j = (g_loss / T) (q_j - a_j)                      j in L
+ *   dl_j = (g_loss / T) q_j                              else, list mode
+ *   dl_j = (g_loss / T) q_j (1 - a_t / q_t)              else, tail mode
+ * mode VS_GRAD_DENSE overwrites dlogits, VS_GRAD_ACCUMULATE adds to it (for
+ * example to vs_score_bwd's); columns at and beyond vocab are left alone.
+ * `args` are those of the forward call.  g_loss [R] fp32 or NULL (= 1). */
+vs_status vs_distill_bwd(const vs_distill_args* args, const void* ctx, const float* g_loss,
+                         void* dlogits, vs_dtype dl_dtype, int64_t grad_ld, int32_t mode,
+                         void* stream);
 
 /* Message describing the last failed call on this thread ("" after success). */
 const char* vs_last_error(void);

@@ -5,6 +5,8 @@ ctypes binding.  PyTorch is used only for device memory and streams."""
 from ._binding import (  # noqa: F401
     LIB_PATH,
     VsError,
+    distill_bwd,
+    distill_fwd,
     fused_lmhead_bwd,
     fused_lmhead_merge,
     fused_lmhead_partial,
@@ -12,11 +14,14 @@ from ._binding import (  # noqa: F401
     l1_distance,
     l1_weight_sum,
     load,
+    sample,
     score_bwd,
     score_fwd,
     support_lmhead_score,
+    topk_logprob,
 )
 from ._binding import (  # noqa: F401
+    ROW_BAD_PARAM,
     ROW_BAD_SUPPORT_ID,
     ROW_DEVICE_TIMEOUT,
     ROW_DUP_SUPPORT_ID,

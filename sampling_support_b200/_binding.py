@@ -23,6 +23,8 @@ VS_GRAD_DENSE, VS_GRAD_ACCUMULATE, VS_GRAD_SPARSE = 0, 1, 2
 VS_CTX_BYTES_PER_ROW = 64
 VS_MAX_SUPPORT_WIDTH = 1024
 VS_MAX_FUSED_TOPK = 64
+VS_MAX_ROW_VOCAB = 1 << 20
+VS_MAX_TOPK = 1024
 
 ROW_TARGET_OUT_OF_RANGE = 1 << 0
 ROW_TARGET_NOT_IN_SUPPORT = 1 << 1
@@ -31,6 +33,7 @@ ROW_DUP_SUPPORT_ID = 1 << 3
 ROW_NONFINITE_INPUT = 1 << 4
 ROW_DEVICE_TIMEOUT = 1 << 5
 ROW_EMPTY_SUPPORT = 1 << 6
+ROW_BAD_PARAM = 1 << 7
 
 _vp = ctypes.c_void_p
 
@@ -55,6 +58,36 @@ class ScoreOut(ctypes.Structure):
         ("entropy_support", _vp), ("valid", _vp), ("status", _vp), ("support_size", _vp),
         ("support_mask", _vp), ("ctx", _vp), ("entropy_sum", _vp), ("valid_count", _vp),
         ("sampled", _vp),
+    ]
+
+
+class SampleArgs(ctypes.Structure):
+    _fields_ = [
+        ("rows", ctypes.c_int32), ("vocab", ctypes.c_int32), ("ld", ctypes.c_int64),
+        ("dtype", ctypes.c_int32), ("logits", _vp),
+        ("temperature", _vp), ("temperature_scalar", ctypes.c_float),
+        ("top_k", _vp), ("top_k_scalar", ctypes.c_int32),
+        ("top_p", _vp), ("top_p_scalar", ctypes.c_float),
+        ("min_p", _vp), ("min_p_scalar", ctypes.c_float),
+        ("uniform", _vp),
+    ]
+
+
+class DistillArgs(ctypes.Structure):
+    _fields_ = [
+        ("rows", ctypes.c_int32), ("vocab", ctypes.c_int32), ("ld", ctypes.c_int64),
+        ("dtype", ctypes.c_int32), ("logits", _vp),
+        ("temperature", _vp), ("temperature_scalar", ctypes.c_float),
+        ("teacher_ids", _vp), ("teacher_logprob", _vp),
+        ("teacher_width", ctypes.c_int32), ("teacher_ld", ctypes.c_int64),
+        ("tail", ctypes.c_int32),
+    ]
+
+
+class DistillOut(ctypes.Structure):
+    _fields_ = [
+        ("loss", _vp), ("valid", _vp), ("status", _vp), ("ctx", _vp), ("g_loss", _vp),
+        ("dlogits", _vp), ("dl_dtype", ctypes.c_int32), ("grad_ld", ctypes.c_int64),
     ]
 
 
@@ -126,6 +159,16 @@ def load() -> ctypes.CDLL:
                                                 ctypes.c_int64, ctypes.c_uint32,
                                                 ctypes.POINTER(ScoreOut), _vp, ctypes.c_int64, _vp]
         lib.vs_support_lmhead_score.restype = i32
+        lib.vs_sample.argtypes = [ctypes.POINTER(SampleArgs), _vp, _vp, _vp, _vp, _vp]
+        lib.vs_sample.restype = i32
+        lib.vs_topk_logprob.argtypes = [i32, i32, ctypes.c_int64, i32, _vp, _vp, ctypes.c_float,
+                                        i32, _vp, _vp, ctypes.c_int64, _vp, _vp]
+        lib.vs_topk_logprob.restype = i32
+        lib.vs_distill_fwd.argtypes = [ctypes.POINTER(DistillArgs), ctypes.POINTER(DistillOut), _vp]
+        lib.vs_distill_fwd.restype = i32
+        lib.vs_distill_bwd.argtypes = [ctypes.POINTER(DistillArgs), _vp, _vp, _vp, i32,
+                                       ctypes.c_int64, i32, _vp]
+        lib.vs_distill_bwd.restype = i32
         lib.vs_last_error.restype = ctypes.c_char_p
         lib.vs_version.restype = ctypes.c_char_p
         _lib = lib
@@ -515,4 +558,215 @@ def support_lmhead_score(hidden, weight, targets, temperature, support_ids, want
                                        VS_WANT_ENTROPY if want_entropy else 0, ctypes.byref(o),
                                        _p(lg), lg.stride(0) if lg is not None else 0,
                                        _stream(stream)))
+    return out
+
+
+class _OnDevice:
+    """Runs a call on its tensors' device and stream: the launch goes to
+    `stream` (default: that device's current stream) with the device current,
+    and tensors taken to a stream other than the current one are recorded on
+    it, so that their memory is not handed out again before the call is done."""
+
+    def __init__(self, device, stream):
+        if device.type != "cuda":
+            raise ValueError(f"tensors must be on a CUDA device, got {device}")
+        self.device, self.guard = device, torch.cuda.device(device)
+        self.stream = stream
+
+    def __enter__(self):
+        self.guard.__enter__()
+        current = torch.cuda.current_stream(self.device)
+        if self.stream is None:
+            self.stream = current
+        self.foreign = self.stream.cuda_stream != current.cuda_stream
+        return self
+
+    def __exit__(self, *exc):
+        return self.guard.__exit__(*exc)
+
+    @property
+    def handle(self):
+        return ctypes.c_void_p(self.stream.cuda_stream)
+
+    def keep(self, *tensors):
+        if self.foreign:
+            for t in tensors:
+                if isinstance(t, torch.Tensor):
+                    t.record_stream(self.stream)
+
+
+def _row_logits(logits, vocab):
+    """(rows, vocab, row stride) of a [rows, ld] logits tensor."""
+    if logits.dim() != 2 or (logits.shape[1] > 1 and logits.stride(1) != 1):
+        raise ValueError("logits must be [rows, ld] with unit stride along the vocabulary")
+    rows, width = logits.shape
+    vocab = width if vocab is None else int(vocab)
+    if vocab > width:
+        raise ValueError(f"vocab {vocab} exceeds the {width} columns of logits")
+    ld = logits.stride(0) if rows > 1 else max(logits.stride(0), width)
+    if rows <= 1:  # the stride of a single row says nothing: round it up to whole vectors
+        per = 16 // logits.element_size()
+        ld = (max(ld, 1) + per - 1) // per * per
+    return rows, vocab, ld
+
+
+def _check_tensor(t, name, shape, dtype, device):
+    if not isinstance(t, torch.Tensor) or t.dtype != dtype or tuple(t.shape) != tuple(shape) \
+            or t.device != device or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {device}")
+
+
+def _row_setting(v, name, rows, dtype, device):
+    """(device tensor or None, scalar) of a per-row setting."""
+    if isinstance(v, torch.Tensor):
+        _check_tensor(v, name, (rows,), dtype, device)
+        return v, 0
+    return None, v
+
+
+def sample(logits, uniform, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0, vocab=None,
+           stream=None):
+    """vs_sample: one token per row of logits [rows, ld] from uniform [rows]
+    (fp32 numbers in [0, 1]).  temperature (0 = greedy), top_k, top_p and min_p
+    are numbers or per-row device tensors (fp32; top_k int32).  Returns
+    {"token", "logprob", "support_size", "status"}; a row without a token holds
+    -1, NaN and 0 (see the header for its status)."""
+    lib = load()
+    dev = logits.device
+    rows, vocab, ld = _row_logits(logits, vocab)
+    _check_tensor(uniform, "uniform", (rows,), torch.float32, dev)
+    t_arr, t_s = _row_setting(temperature, "temperature", rows, torch.float32, dev)
+    k_arr, k_s = _row_setting(top_k, "top_k", rows, torch.int32, dev)
+    p_arr, p_s = _row_setting(top_p, "top_p", rows, torch.float32, dev)
+    m_arr, m_s = _row_setting(min_p, "min_p", rows, torch.float32, dev)
+    a = SampleArgs(rows=rows, vocab=vocab, ld=ld, dtype=_dtype_code(logits), logits=logits.data_ptr(),
+                   temperature=None if t_arr is None else t_arr.data_ptr(), temperature_scalar=float(t_s),
+                   top_k=None if k_arr is None else k_arr.data_ptr(), top_k_scalar=int(k_s),
+                   top_p=None if p_arr is None else p_arr.data_ptr(), top_p_scalar=float(p_s),
+                   min_p=None if m_arr is None else m_arr.data_ptr(), min_p_scalar=float(m_s),
+                   uniform=uniform.data_ptr())
+    with _OnDevice(dev, stream) as on:
+        out = {"token": torch.empty(rows, dtype=torch.int32, device=dev),
+               "logprob": torch.empty(rows, dtype=torch.float32, device=dev),
+               "support_size": torch.empty(rows, dtype=torch.int32, device=dev),
+               "status": torch.empty(rows, dtype=torch.int32, device=dev)}
+        _check(lib.vs_sample(ctypes.byref(a), _p(out["token"]), _p(out["logprob"]),
+                             _p(out["support_size"]), _p(out["status"]), on.handle))
+        on.keep(logits, uniform, t_arr, k_arr, p_arr, m_arr, *out.values())
+    return out
+
+
+def topk_logprob(logits, k, temperature=1.0, vocab=None, stream=None):
+    """vs_topk_logprob: the first k tokens of each row (logit descending, token
+    id ascending) and their log-probabilities over the row: {"ids" [rows, k]
+    int32, "logprob" [rows, k] fp32, "status"}; -1 and -inf past a row's
+    unmasked tokens."""
+    lib = load()
+    dev = logits.device
+    rows, vocab, ld = _row_logits(logits, vocab)
+    t_arr, t_s = _row_setting(temperature, "temperature", rows, torch.float32, dev)
+    k = int(k)
+    with _OnDevice(dev, stream) as on:
+        out = {"ids": torch.empty((rows, max(k, 0)), dtype=torch.int32, device=dev),
+               "logprob": torch.empty((rows, max(k, 0)), dtype=torch.float32, device=dev),
+               "status": torch.empty(rows, dtype=torch.int32, device=dev)}
+        _check(lib.vs_topk_logprob(rows, vocab, ld, _dtype_code(logits), _p(logits), _p(t_arr),
+                                   float(t_s), k, _p(out["ids"]), _p(out["logprob"]), k,
+                                   _p(out["status"]), on.handle))
+        on.keep(logits, t_arr, *out.values())
+    return out
+
+
+def _distill_args(logits, teacher_ids, teacher_logprob, temperature, tail, vocab):
+    dev = logits.device
+    rows, vocab, ld = _row_logits(logits, vocab)
+    for t, name, dtype in ((teacher_ids, "teacher_ids", torch.int32),
+                           (teacher_logprob, "teacher_logprob", torch.float32)):
+        if t.dim() != 2 or t.shape[0] != rows or t.dtype != dtype or t.device != dev \
+                or (t.shape[1] > 1 and t.stride(1) != 1):
+            raise ValueError(f"{name} must be a {dtype} tensor [rows, width] on {dev}, unit stride in a row")
+    width = teacher_ids.shape[1]
+    if teacher_logprob.shape[1] != width or (rows > 1 and teacher_logprob.stride(0) != teacher_ids.stride(0)):
+        raise ValueError("teacher_ids and teacher_logprob must have the same shape and row stride")
+    t_arr, t_s = _row_setting(temperature, "temperature", rows, torch.float32, dev)
+    return DistillArgs(rows=rows, vocab=vocab, ld=ld, dtype=_dtype_code(logits), logits=logits.data_ptr(),
+                       temperature=None if t_arr is None else t_arr.data_ptr(),
+                       temperature_scalar=float(t_s), teacher_ids=teacher_ids.data_ptr(),
+                       teacher_logprob=teacher_logprob.data_ptr(), teacher_width=width,
+                       teacher_ld=max(teacher_ids.stride(0), width) if rows > 1 else width,
+                       tail=1 if tail else 0), t_arr
+
+
+def _grad_like(rows, vocab, dtype, device):
+    if dtype not in (torch.float32, torch.bfloat16):
+        raise TypeError(f"grad_dtype must be float32 or bfloat16, got {dtype}")
+    return torch.empty((rows, (vocab + 7) // 8 * 8), dtype=dtype, device=device)
+
+
+def distill_fwd(logits, teacher_ids, teacher_logprob, temperature=1.0, tail=False, want_grad=False,
+                g_loss=None, grad_dtype=None, vocab=None, stream=None):
+    """vs_distill_fwd: {"loss", "valid", "status"} per row of the student's
+    logits against the teacher's list (int32 ids, -1 padded, and fp32
+    log-probabilities, as topk_logprob or fused_lmhead_score return them).
+    tail=False renormalises the teacher over its list, tail=True keeps its
+    remaining mass as one more outcome.  want_grad adds "ctx" for distill_bwd.
+    grad_dtype (with g_loss [rows] fp32, default ones) adds "grad", the
+    gradient of sum g_loss * loss, in the same pass: [rows, vocab rounded up
+    to 8], columns beyond vocab unwritten."""
+    lib = load()
+    dev = logits.device
+    a, t_arr = _distill_args(logits, teacher_ids, teacher_logprob, temperature, tail, vocab)
+    rows = a.rows
+    if g_loss is not None:
+        _check_tensor(g_loss, "g_loss", (rows,), torch.float32, dev)
+        if grad_dtype is None:
+            raise ValueError("g_loss needs grad_dtype")
+    with _OnDevice(dev, stream) as on:
+        out = {"loss": torch.empty(rows, dtype=torch.float32, device=dev),
+               "valid": torch.empty(rows, dtype=torch.uint8, device=dev),
+               "status": torch.empty(rows, dtype=torch.int32, device=dev)}
+        if want_grad:
+            out["ctx"] = torch.empty((rows, VS_CTX_BYTES_PER_ROW), dtype=torch.uint8, device=dev)
+        if grad_dtype is not None:
+            out["grad"] = _grad_like(rows, a.vocab, grad_dtype, dev)
+        g = out.get("grad")
+        o = DistillOut(loss=out["loss"].data_ptr(), valid=out["valid"].data_ptr(),
+                       status=out["status"].data_ptr(),
+                       ctx=out["ctx"].data_ptr() if want_grad else None,
+                       g_loss=None if g_loss is None else g_loss.data_ptr(),
+                       dlogits=None if g is None else g.data_ptr(),
+                       dl_dtype=VS_BF16 if grad_dtype == torch.bfloat16 else VS_F32,
+                       grad_ld=0 if g is None else g.shape[1])
+        _check(lib.vs_distill_fwd(ctypes.byref(a), ctypes.byref(o), on.handle))
+        on.keep(logits, teacher_ids, teacher_logprob, t_arr, g_loss, *out.values())
+    return out
+
+
+def distill_bwd(logits, teacher_ids, teacher_logprob, ctx, g_loss=None, temperature=1.0, tail=False,
+                grad_dtype=torch.float32, mode=VS_GRAD_DENSE, out=None, vocab=None, stream=None):
+    """vs_distill_bwd from a distill_fwd(..., want_grad=True) result's "ctx" and
+    the same inputs; returns dlogits [rows, vocab rounded up to 8] (or `out`,
+    overwritten or, with VS_GRAD_ACCUMULATE, added to)."""
+    lib = load()
+    dev = logits.device
+    a, t_arr = _distill_args(logits, teacher_ids, teacher_logprob, temperature, tail, vocab)
+    _check_tensor(ctx, "ctx", (a.rows, VS_CTX_BYTES_PER_ROW), torch.uint8, dev)
+    if g_loss is not None:
+        _check_tensor(g_loss, "g_loss", (a.rows,), torch.float32, dev)
+    if out is None and mode == VS_GRAD_ACCUMULATE:
+        raise ValueError("VS_GRAD_ACCUMULATE needs out")
+    with _OnDevice(dev, stream) as on:
+        if out is None:
+            out = _grad_like(a.rows, a.vocab, grad_dtype, dev)
+        if out.dim() != 2 or out.shape[0] != a.rows or out.shape[1] < a.vocab or out.device != dev \
+                or out.dtype not in (torch.float32, torch.bfloat16) or out.stride(1) != 1:
+            raise ValueError("out must be a float32 or bfloat16 [rows, >= vocab] tensor beside logits")
+        ld = out.stride(0)
+        if a.rows == 1:
+            per = 16 // out.element_size()
+            ld = (max(ld, a.vocab) + per - 1) // per * per
+        _check(lib.vs_distill_bwd(ctypes.byref(a), _p(ctx), _p(g_loss), _p(out),
+                                  VS_BF16 if out.dtype == torch.bfloat16 else VS_F32, ld, mode,
+                                  on.handle))
+        on.keep(logits, teacher_ids, teacher_logprob, t_arr, ctx, g_loss, out)
     return out

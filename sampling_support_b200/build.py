@@ -13,7 +13,8 @@ CSRC = PKG / "csrc"
 INCLUDE = PKG.parent / "include"
 LIB = PKG / "libvs.so"
 
-SOURCES = ["api.cu", "score_fwd.cu", "score_row.cu", "score_bwd.cu", "l1_distance.cu", "fused_lmhead.cu", "support_head.cu"]
+SOURCES = ["api.cu", "score_fwd.cu", "score_row.cu", "score_bwd.cu", "l1_distance.cu", "fused_lmhead.cu", "support_head.cu",
+           "sample.cu", "distill.cu"]
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 
 

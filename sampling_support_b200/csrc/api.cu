@@ -465,3 +465,203 @@ vs_status vs_support_lmhead_score(int32_t rows, int32_t vocab, int32_t hidden_di
 }
 
 }  // extern "C"
+
+namespace {
+
+// vocab * 2^shift <= 2^63
+int row_fx_shift(int32_t vocab) {
+  int bits = 0;
+  while ((1ll << bits) < static_cast<long long>(vocab)) ++bits;
+  return 62 - bits;
+}
+
+// Checks shared by the row operators below.
+vs_status check_rows(int32_t rows, int32_t vocab, int64_t ld, vs_dtype dtype, const void* logits) {
+  if (rows < 0) return fail(VS_ERR_INVALID_ARG, "rows must be >= 0");
+  if (vocab < 1) return fail(VS_ERR_INVALID_ARG, "vocab must be >= 1");
+  if (vocab > VS_MAX_ROW_VOCAB) return fail(VS_ERR_UNSUPPORTED, "vocab exceeds VS_MAX_ROW_VOCAB");
+  if (ld < vocab) return fail(VS_ERR_INVALID_ARG, "ld must be >= vocab");
+  if (dtype != VS_F32 && dtype != VS_BF16)
+    return fail(VS_ERR_INVALID_ARG, "dtype must be VS_BF16 or VS_F32");
+  if (rows == 0) return VS_OK;
+  if (rows > (1 << 27)) return fail(VS_ERR_UNSUPPORTED, "rows must be at most 2^27");
+  if (!logits || !aligned16(logits))
+    return fail(VS_ERR_INVALID_ARG, "logits must be non-NULL and 16-byte aligned");
+  if ((static_cast<uint64_t>(ld) * esize(dtype)) % 16 != 0)
+    return fail(VS_ERR_INVALID_ARG, "ld * sizeof(element) must be a multiple of 16 bytes");
+  return VS_OK;
+}
+
+vs_status check_distill(const vs_distill_args* a) {
+  if (!a) return fail(VS_ERR_INVALID_ARG, "args is NULL");
+  const vs_status st = check_rows(a->rows, a->vocab, a->ld, a->dtype, a->logits);
+  if (st != VS_OK) return st;
+  if (a->teacher_width < 0 || a->teacher_width > VS_MAX_SUPPORT_WIDTH)
+    return fail(VS_ERR_UNSUPPORTED, "teacher_width must lie in [0, VS_MAX_SUPPORT_WIDTH]");
+  if (a->teacher_ld < a->teacher_width)
+    return fail(VS_ERR_INVALID_ARG, "teacher_ld must be >= teacher_width");
+  if (a->tail != 0 && a->tail != 1) return fail(VS_ERR_INVALID_ARG, "tail must be 0 or 1");
+  if (!a->temperature && !(std::isfinite(a->temperature_scalar) && a->temperature_scalar > 0.f))
+    return fail(VS_ERR_INVALID_ARG, "temperature_scalar must be finite and > 0");
+  if (a->rows > 0 && a->teacher_width > 0 && (!a->teacher_ids || !a->teacher_logprob))
+    return fail(VS_ERR_INVALID_ARG, "teacher_ids and teacher_logprob must be non-NULL");
+  return VS_OK;
+}
+
+// A gradient output [rows, grad_ld] beside the logits it belongs to.
+vs_status check_grad(const vs_distill_args* a, const void* dlogits, vs_dtype dl_dtype,
+                     int64_t grad_ld) {
+  if (dl_dtype != VS_F32 && dl_dtype != VS_BF16)
+    return fail(VS_ERR_INVALID_ARG, "dl_dtype must be VS_BF16 or VS_F32");
+  if (!dlogits || !aligned16(dlogits))
+    return fail(VS_ERR_INVALID_ARG, "dlogits must be non-NULL and 16-byte aligned");
+  if (grad_ld < a->vocab) return fail(VS_ERR_INVALID_ARG, "grad_ld must be >= vocab");
+  if ((static_cast<uint64_t>(grad_ld) * esize(dl_dtype)) % 16 != 0)
+    return fail(VS_ERR_INVALID_ARG, "grad_ld * sizeof(element) must be a multiple of 16 bytes");
+  const uintptr_t l0 = reinterpret_cast<uintptr_t>(a->logits), g0 = reinterpret_cast<uintptr_t>(dlogits);
+  const uintptr_t rows = static_cast<uintptr_t>(a->rows);
+  const uintptr_t l1 = l0 + ((rows - 1) * static_cast<uintptr_t>(a->ld) + a->vocab) * esize(a->dtype);
+  const uintptr_t g1 = g0 + ((rows - 1) * static_cast<uintptr_t>(grad_ld) + a->vocab) * esize(dl_dtype);
+  if (l0 < g1 && g0 < l1) return fail(VS_ERR_INVALID_ARG, "dlogits must not overlap logits");
+  return VS_OK;
+}
+
+vs::DistillParams distill_params(const vs_distill_args* a) {
+  vs::DistillParams p{};
+  p.rows = a->rows;
+  p.vocab = a->vocab;
+  p.width = a->teacher_width;
+  p.tail = a->tail;
+  p.ld = a->ld;
+  p.teacher_ld = a->teacher_ld;
+  p.logits = a->logits;
+  p.temperature = a->temperature;
+  p.temperature_scalar = a->temperature_scalar;
+  p.ids = a->teacher_ids;
+  p.lp = a->teacher_logprob;
+  return p;
+}
+
+}  // namespace
+
+extern "C" {
+
+vs_status vs_sample(const vs_sample_args* a, int32_t* token, float* logprob, int32_t* support_size,
+                    uint32_t* status, void* stream) {
+  if (!a) return fail(VS_ERR_INVALID_ARG, "args is NULL");
+  const vs_status st = check_rows(a->rows, a->vocab, a->ld, a->dtype, a->logits);
+  if (st != VS_OK) return st;
+  if (!a->temperature && !(std::isfinite(a->temperature_scalar) && a->temperature_scalar >= 0.f))
+    return fail(VS_ERR_INVALID_ARG, "temperature_scalar must be finite and >= 0");
+  if (!a->top_p && !(a->top_p_scalar > 0.f && a->top_p_scalar <= 1.f))
+    return fail(VS_ERR_INVALID_ARG, "top_p_scalar must lie in (0, 1]");
+  if (!a->min_p && !(a->min_p_scalar >= 0.f && a->min_p_scalar < 1.f))
+    return fail(VS_ERR_INVALID_ARG, "min_p_scalar must lie in [0, 1)");
+  if (a->rows == 0) return ok();
+  if (!a->uniform) return fail(VS_ERR_INVALID_ARG, "uniform is NULL");
+  if (!token) return fail(VS_ERR_INVALID_ARG, "token is NULL");
+  vs::SampleParams p{};
+  p.rows = a->rows;
+  p.vocab = a->vocab;
+  p.ld = a->ld;
+  p.logits = a->logits;
+  p.temperature = a->temperature;
+  p.temperature_scalar = a->temperature_scalar;
+  p.top_k = a->top_k;
+  p.top_k_scalar = a->top_k_scalar;
+  p.top_p = a->top_p;
+  p.top_p_scalar = a->top_p_scalar;
+  p.min_p = a->min_p;
+  p.min_p_scalar = a->min_p_scalar;
+  p.uniform = a->uniform;
+  p.token = token;
+  p.logprob = logprob;
+  p.support_size = support_size;
+  p.status = status;
+  p.fx_shift = row_fx_shift(a->vocab);
+  const cudaError_t e = vs::launch_sample(p, a->dtype, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "vs_sample launch");
+  return ok();
+}
+
+vs_status vs_topk_logprob(int32_t rows, int32_t vocab, int64_t ld, vs_dtype dtype,
+                          const void* logits, const float* temperature, float temperature_scalar,
+                          int32_t k, int32_t* ids, float* logprob, int64_t out_ld,
+                          uint32_t* status, void* stream) {
+  const vs_status st = check_rows(rows, vocab, ld, dtype, logits);
+  if (st != VS_OK) return st;
+  if (!temperature && !(std::isfinite(temperature_scalar) && temperature_scalar > 0.f))
+    return fail(VS_ERR_INVALID_ARG, "temperature_scalar must be finite and > 0");
+  if (k < 1 || k > vocab) return fail(VS_ERR_INVALID_ARG, "k must lie in [1, vocab]");
+  if (k > VS_MAX_TOPK) return fail(VS_ERR_UNSUPPORTED, "k exceeds VS_MAX_TOPK");
+  if (out_ld < k) return fail(VS_ERR_INVALID_ARG, "out_ld must be >= k");
+  if (rows == 0) return ok();
+  if (!ids) return fail(VS_ERR_INVALID_ARG, "ids is NULL");
+  vs::TopkParams p{};
+  p.rows = rows;
+  p.vocab = vocab;
+  p.k = k;
+  p.ld = ld;
+  p.out_ld = out_ld;
+  p.logits = logits;
+  p.temperature = temperature;
+  p.temperature_scalar = temperature_scalar;
+  p.ids = ids;
+  p.logprob = logprob;
+  p.status = status;
+  p.fx_shift = row_fx_shift(vocab);
+  const cudaError_t e = vs::launch_topk(p, dtype, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "vs_topk_logprob launch");
+  return ok();
+}
+
+vs_status vs_distill_fwd(const vs_distill_args* a, const vs_distill_out* o, void* stream) {
+  vs_status st = check_distill(a);
+  if (st != VS_OK) return st;
+  if (!o) return fail(VS_ERR_INVALID_ARG, "out is NULL");
+  if (a->rows == 0) return ok();
+  if (o->ctx && !aligned16(o->ctx)) return fail(VS_ERR_INVALID_ARG, "ctx must be 16-byte aligned");
+  if (o->dlogits) {
+    st = check_grad(a, o->dlogits, o->dl_dtype, o->grad_ld);
+    if (st != VS_OK) return st;
+  } else if (o->g_loss) {
+    return fail(VS_ERR_INVALID_ARG, "g_loss needs dlogits");
+  }
+  vs::DistillParams p = distill_params(a);
+  p.loss = o->loss;
+  p.valid = o->valid;
+  p.status = o->status;
+  p.ctx = o->ctx;
+  p.g_loss = o->g_loss;
+  p.dlogits = o->dlogits;
+  p.grad_ld = o->grad_ld;
+  const cudaError_t e = vs::launch_distill_fwd(p, a->dtype, o->dlogits ? o->dl_dtype : VS_F32,
+                                               static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "vs_distill_fwd launch");
+  return ok();
+}
+
+vs_status vs_distill_bwd(const vs_distill_args* a, const void* ctx, const float* g_loss,
+                         void* dlogits, vs_dtype dl_dtype, int64_t grad_ld, int32_t mode,
+                         void* stream) {
+  vs_status st = check_distill(a);
+  if (st != VS_OK) return st;
+  if (mode != VS_GRAD_DENSE && mode != VS_GRAD_ACCUMULATE)
+    return fail(VS_ERR_INVALID_ARG, "mode must be VS_GRAD_DENSE or VS_GRAD_ACCUMULATE");
+  if (a->rows == 0) return ok();
+  if (!ctx || !aligned16(ctx))
+    return fail(VS_ERR_INVALID_ARG, "ctx must be non-NULL and 16-byte aligned");
+  st = check_grad(a, dlogits, dl_dtype, grad_ld);
+  if (st != VS_OK) return st;
+  vs::DistillParams p = distill_params(a);
+  p.ctx = const_cast<void*>(ctx);
+  p.g_loss = g_loss;
+  p.dlogits = dlogits;
+  p.grad_ld = grad_ld;
+  const cudaError_t e = vs::launch_distill_bwd(p, a->dtype, dl_dtype, mode == VS_GRAD_ACCUMULATE,
+                                               static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "vs_distill_bwd launch");
+  return ok();
+}
+
+}  // extern "C"

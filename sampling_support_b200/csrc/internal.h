@@ -92,7 +92,65 @@ struct BwdParams {
   int32_t chunk;  // elements per CTA (multiple of 32); == padded vocab when whole rows
 };
 
+// Sampling from given uniform numbers.
+struct SampleParams {
+  int32_t rows, vocab;
+  int64_t ld;
+  const void* logits;
+  const float* temperature;
+  float temperature_scalar;
+  const int32_t* top_k;
+  int32_t top_k_scalar;
+  const float* top_p;
+  float top_p_scalar;
+  const float* min_p;
+  float min_p_scalar;
+  const float* uniform;
+  int32_t* token;
+  float* logprob;
+  int32_t* support_size;
+  uint32_t* status;
+  int32_t fx_shift;  // fixed-point scale of the masses: vocab * 2^fx_shift <= 2^63
+};
+
+struct TopkParams {
+  int32_t rows, vocab, k;
+  int64_t ld, out_ld;
+  const void* logits;
+  const float* temperature;
+  float temperature_scalar;
+  int32_t* ids;
+  float* logprob;
+  uint32_t* status;
+  int32_t fx_shift;
+};
+
+struct DistillParams {
+  int32_t rows, vocab, width, tail;
+  int64_t ld, teacher_ld, grad_ld;
+  const void* logits;
+  const float* temperature;
+  float temperature_scalar;
+  const int32_t* ids;
+  const float* lp;
+  float* loss;
+  uint8_t* valid;
+  uint32_t* status;
+  void* ctx;
+  const float* g_loss;
+  void* dlogits;
+  int32_t chunk;  // elements per CTA (multiple of 32)
+};
+
+// CTAs of the cluster that shares one row.
+int row_cluster_size(int rows, int vocab);
+
 // launchers (return a cudaError_t from the launch)
+cudaError_t launch_sample(const SampleParams& p, vs_dtype dtype, cudaStream_t s);
+cudaError_t launch_topk(const TopkParams& p, vs_dtype dtype, cudaStream_t s);
+cudaError_t launch_distill_fwd(DistillParams p, vs_dtype dtype, vs_dtype dl_dtype, cudaStream_t s);
+cudaError_t launch_distill_bwd(DistillParams p, vs_dtype dtype, vs_dtype dl_dtype, bool accumulate,
+                               cudaStream_t s);
 cudaError_t launch_score_computed(const ScoreParams& p, vs_dtype dtype, cudaStream_t s);
 // Recorded supports.  Lists of up to 64 ids need a workspace of
 // score_recorded_workspace_bytes (16-byte aligned); wider lists none.
