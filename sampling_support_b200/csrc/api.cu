@@ -2,6 +2,7 @@
 // Every check runs on the host before anything is enqueued; nothing here
 // allocates device memory.
 
+#include <algorithm>
 #include <cmath>
 #include <cstdio>
 #include <string>
@@ -472,7 +473,7 @@ namespace {
 int row_fx_shift(int32_t vocab) {
   int bits = 0;
   while ((1ll << bits) < static_cast<long long>(vocab)) ++bits;
-  return 62 - bits;
+  return std::min(50, 62 - bits);  // and w 2^shift + 2^52 has to keep its integer bits
 }
 
 // Checks shared by the row operators below.

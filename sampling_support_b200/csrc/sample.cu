@@ -13,8 +13,8 @@ namespace vs {
 
 namespace {
 
-// Largest top-k taken through the list of candidates above a floor (the
-// k-th largest of the threads' maxima needs k of the 1,024 threads).
+// Largest top-k taken through the list of candidates above a floor (half of
+// the threads' 1,024 maxima: beyond it the floor is far below the k-th).
 constexpr int kListTopK = 512;
 
 __device__ __forceinline__ void write_none(const SampleParams& P, int row, uint32_t status) {
@@ -39,143 +39,444 @@ __device__ __forceinline__ u64 draw_target(float u, u64 mass) {
   return t < mass ? t : mass;
 }
 
+// Leader: the support's cut and the drawn token from a list that holds at
+// least the first nk tokens of the row.  The block sorts and takes the masses;
+// its first warp decides.
 template <typename Raw>
-__global__ void __launch_bounds__(kRsThreads, 1) sample_kernel(SampleParams P) {
-  extern __shared__ __align__(16) unsigned char rs_smem[];
-  RsShared& sh = *reinterpret_cast<RsShared*>(rs_smem);
-  __shared__ u64 s_mass;
-  RsRow<Raw> R;
-  const int row = static_cast<int>(blockIdx.x / cg::this_cluster().num_blocks());
-  R.init(P.logits, row, P.ld, P.vocab, &sh);
-  const bool lead = R.rank == 0 && threadIdx.x == 0;
-
-  float t = P.temperature ? P.temperature[row] : P.temperature_scalar;
-  int k = P.top_k ? P.top_k[row] : P.top_k_scalar;
-  float p = P.top_p ? P.top_p[row] : P.top_p_scalar;
-  float m = P.min_p ? P.min_p[row] : P.min_p_scalar;
-  const float u = P.uniform[row];
-  const bool fine = t >= 0.f && t < kInf && p > 0.f && m <= 1.f && u >= 0.f && u <= 1.f;
-
-  uint32_t kmax, kmin, thread_max;
-  const bool finite = rs_extremes(R, kmax, kmin, thread_max);
-  if (!finite || !fine || kmax <= RsRow<Raw>::kMaskedKey) {
-    if (lead)
-      write_none(P, row, (finite ? 0u : VS_ROW_NONFINITE_INPUT) | (fine ? 0u : VS_ROW_BAD_PARAM) |
-                             (finite && kmax <= RsRow<Raw>::kMaskedKey ? VS_ROW_EMPTY_SUPPORT : 0u));
-    R.sync();  // peers read this CTA's extremes
-    return;
+__device__ __forceinline__ void draw_from_list(const SampleParams& P, int row, const Settings& s, uint32_t n_list) {
+  RsShared& sh = rs_shared();
+  const RsMass M = sh.M;
+  const uint32_t nk = min(static_cast<uint32_t>(s.k), n_list);
+  rs_sort(n_list, nk);
+  rs_list_masses<Raw>(sh, nk);
+  if (threadIdx.x >= 32) return;
+  const int lane = threadIdx.x;
+  u64 mass = 0ull;
+  for (uint32_t i = lane; i < nk; i += 32) mass += sh.list[i];
+  mass = rs_warp_sum(mass);
+  uint32_t n = nk;
+  if (s.p < 1.f) {
+    u64 m = 0ull;
+    n = rs_list_cross(sh, nk, topp_target(s.p, static_cast<double>(mass)), m) + 1u;
+    mass = m;
   }
-  if (t == 0.f) {  // greedy: the first token of the order
-    t = 1.f;
-    k = 1;
-    p = 1.f;
-    m = 0.f;
-  }
-  RsMass M;
-  M.vmax = static_cast<double>(KeyTraits<Raw>::decode(kmax));
-  M.inv_t = 1.0 / static_cast<double>(t);
-  M.scale = static_cast<double>(1ull << P.fx_shift);
-
-  if (k > 0 && k < P.vocab && k <= kListTopK) {
-    const uint32_t floor_key = max(rs_topk_floor(R, thread_max, k), RsRow<Raw>::kMaskedKey + 1u);
-    const uint32_t n_list = rs_collect(R, floor_key, kmax);
-    if (n_list <= static_cast<uint32_t>(kRsCap)) {
-      if (R.rank == 0) {
-        const uint32_t nk = min(static_cast<uint32_t>(k), n_list);
-        rs_sort(sh, n_list, nk);
-        const uint32_t i = threadIdx.x;
-        float v = 0.f;
-        u64 w = 0ull;
-        double wd = 0.0;
-        if (i < nk) {
-          v = KeyTraits<Raw>::decode(static_cast<uint32_t>(sh.sorted[i] >> 32));
-          wd = exp(M.z(v));
-          w = M.fx(v);
-        }
-        u64 upto, none;
-        rs_scan(w, 0ull, upto, none, sh);
-        upto += w;
-        if (i == nk - 1) s_mass = upto;
-        cta_sync();
-        const u64 zk = s_mass;
-        uint32_t n = nk;
-        if (p < 1.f) {
-          const u64 want = topp_target(p, static_cast<double>(zk));
-          n = min(n, static_cast<uint32_t>(__syncthreads_count(i < nk && upto < want)) + 1u);
-        }
-        if (m > 0.f)
-          n = min(n, static_cast<uint32_t>(__syncthreads_count(i < nk && wd >= static_cast<double>(m))));
-        cta_sync();
-        if (i == n - 1) s_mass = upto;
-        cta_sync();
-        const u64 zs = s_mass, want = draw_target(u, zs);
-        if (i < n && upto - w < want && want <= upto) {
-          P.token[row] = static_cast<int32_t>(~static_cast<uint32_t>(sh.sorted[i]));
-          write_row(P, row, M.z(v), zs, n, M);
-        }
-      }
-      return;  // rs_collect ended with a cluster barrier: nothing is read from peers after it
-    }
-  }
-
-  RsBins B;
-  B.vmax = KeyTraits<Raw>::decode(kmax);
-  {
-    // bins over the values whose mass is not zero in fixed point (46 nats), or over the row's own range
-    const float range = fminf(B.vmax - KeyTraits<Raw>::decode(kmin), 46.f * t);
-    B.s = range > 0.f ? fminf(static_cast<float>(kRsBins - 1) / range, 1e38f) : 0.f;
-  }
-  rs_hist(R, M, kRsBins, sh.rcnt, sh.rmass, [&](uint32_t, float v) { return B.of(v); });
-  const RsMsg all = R.broadcast([&](RsMsg* msg) {
-    if (threadIdx.x == 0) {
-      msg->cnt = sh.rcnt[kRsBins - 1];
-      msg->mass = sh.rmass[kRsBins - 1];
-    }
-  });
-  u64 n = all.cnt, mass = all.mass;
-  uint32_t last = kmin;  // the key that the support reaches down to
-  if (k > 0 && static_cast<u64>(k) < n) {
-    const RsHit h = rs_find(R, M, B, kmin, kmax, false, static_cast<u64>(k));
-    n = h.cnt;
-    mass = h.mass;
-    last = h.key;
-  }
-  if (p < 1.f) {
-    const RsHit h = rs_find(R, M, B, kmin, kmax, true, topp_target(p, static_cast<double>(mass)));
-    if (h.cnt < n) {
-      n = h.cnt;
-      mass = h.mass;
-      last = h.key;
-    }
-  }
-  if (m > 0.f) {
-    uint32_t lo = kmin, hi = kmax;  // the smallest key with w >= min_p
-    while (lo < hi) {
-      const uint32_t mid = lo + ((hi - lo) >> 1);
-      if (exp(M.z(KeyTraits<Raw>::decode(mid))) >= static_cast<double>(m))
-        hi = mid;
-      else
-        lo = mid + 1;
-    }
-    if (lo > last) {
-      u64 cnt, above;
-      rs_sum_above(R, M, lo, cnt, above);
-      if (cnt < n) {
-        n = cnt;
-        mass = above;
+  if (s.m > 0.f) {
+    uint32_t keep = 0u;  // the order is by mass: those kept are the first ones
+    u64 m = 0ull;
+    for (uint32_t i = lane; i < n; i += 32) {
+      const float v = KeyTraits<Raw>::decode(static_cast<uint32_t>(sh.sorted[i] >> 32));
+      if (M.w(v) >= static_cast<double>(s.m)) {
+        ++keep;
+        m += sh.list[i];
       }
     }
+    n = __reduce_add_sync(0xffffffffu, keep);
+    mass = rs_warp_sum(m);
   }
-  const RsHit h = rs_find(R, M, B, kmin, kmax, true, draw_target(u, mass));
-  if (h.tie)
-    rs_ties(R, h.key, h.tie, [&](int id, u64 at) {
-      if (at == h.tie - 1) P.token[row] = id;
+  u64 upto = 0ull;
+  const uint32_t at = rs_list_cross(sh, n, draw_target(s.u, mass), upto);
+  if (lane == 0) {
+    const u64 e = sh.sorted[at];
+    P.token[row] = static_cast<int32_t>(~static_cast<uint32_t>(e));
+    write_row(P, row, M.z(KeyTraits<Raw>::decode(static_cast<uint32_t>(e >> 32))), mass, n, M);
+  }
+}
+
+// The smallest key in [lo, hi] whose mass is at least m (w(hi) >= m): the
+// lanes of one warp test 32 keys at a time.
+template <typename Raw>
+__device__ __forceinline__ uint32_t first_above(const RsMass& M, float m, uint32_t lo, uint32_t hi) {
+  const int lane = threadIdx.x & 31;
+  while (lo < hi) {
+    const uint32_t step = (hi - lo) / 32u + 1u;
+    const uint32_t off = min(hi - lo, lane * step);
+    const uint32_t yes = __ballot_sync(0xffffffffu, M.w(KeyTraits<Raw>::decode(lo + off)) >= static_cast<double>(m));
+    const int l = yes ? __ffs(yes) - 1 : 32;  // hi itself passes
+    const uint32_t top = l == 32 ? hi : lo + min(hi - lo, l * step);
+    lo = l == 0 ? lo : lo + min(hi - lo, (l - 1) * step) + 1u;
+    hi = top;
+    if (lo > hi) lo = hi;
+  }
+  return lo;
+}
+
+// One step of the leader's first warp: takes what the last request brought,
+// goes on through the cuts (top-k, top-p, min-p, the draw) and fills the next
+// request.  Each cut names a bin from the running sums; where the bin does not
+// decide by itself, the cluster is asked to list its elements, to zoom into it
+// when they are too many, or to add up a part of it.  ONE: every bin holds one
+// value, whose tokens have one mass and follow one another in the order, so
+// the place inside it is arithmetic.
+template <typename Raw, bool ONE>
+__device__ __noinline__ void draw_step(RsMsg* out) {
+  RsShared& sh = rs_shared();
+  const int lane = threadIdx.x & 31;
+  RsDraw& d = sh.draw;
+  const RsMass M = sh.M;
+  const Settings s = d.s;
+  int phase = d.phase;
+  u64 n = d.n, mass = d.mass, t = d.t;
+  bool by_mass = d.by_mass != 0u;
+  uint32_t klo = d.klo, khi = d.khi, asked = d.asked;
+  RsBin f = d.f;
+
+  RsMsg q{kRsStop, 0u, 0u, 0u, 0ull, 0ull};
+  bool found = false, open = false;      // an element is known; a range is under search
+  u64 cnt = 0ull, sum = 0ull, tie = 0ull;  // the sums through the element, its place in its group
+  uint32_t key = 0u;
+  int32_t id = -1;
+  if (asked == kRsCollect) {
+    uint32_t at;
+    sum = f.mass;
+    if (by_mass)
+      at = rs_list_cross(sh, static_cast<uint32_t>(f.n), t, sum);
+    else {
+      at = min(static_cast<uint32_t>(t - f.cnt) - 1u, static_cast<uint32_t>(kRsCap - 1));
+      u64 m = 0ull;
+      for (uint32_t i = lane; i <= at; i += 32) m += sh.list[i];
+      sum += rs_warp_sum(m);
+    }
+    found = true;
+    cnt = f.cnt + at + 1u;
+    key = static_cast<uint32_t>(sh.sorted[at] >> 32);
+    id = static_cast<int32_t>(~static_cast<uint32_t>(sh.sorted[at]));
+  } else if (asked == kRsZoom) {
+    int shift = 0;
+    while (((khi - klo) >> shift) >= static_cast<uint32_t>(kRsZoomBins)) ++shift;
+    f = rs_find_zoom(sh, by_mass, t, f.cnt, f.mass);
+    const uint32_t top = khi - (static_cast<uint32_t>(f.bin) << shift), width = (1u << shift) - 1u;
+    klo = top - klo > width ? top - width : klo;
+    khi = top;
+    open = true;
+  } else if (asked == kRsSum) {
+    if (f.cnt + d.got_cnt < n) {
+      n = f.cnt + d.got_cnt;
+      mass = f.mass + d.got_mass;
+    }
+    phase = 3;
+  }
+  asked = kRsStop;
+  while (asked == kRsStop) {
+    if (!found && !open) {  // the next cut's bin
+      if (phase == 0) {
+        if (!(s.k > 0 && static_cast<u64>(s.k) < n)) {
+          phase = 1;
+          continue;
+        }
+        by_mass = false;
+        t = static_cast<u64>(s.k);
+      } else if (phase == 1) {
+        if (!(s.p < 1.f)) {
+          phase = 2;
+          continue;
+        }
+        by_mass = true;
+        t = topp_target(s.p, static_cast<double>(mass));
+      } else if (phase == 2) {
+        phase = 3;
+        if (!(s.m > 0.f)) continue;
+        // the first bin that does not pass whole, from the maximum's on (no mass is
+        // asked for above the maximum, where there is none)
+        const float top = static_cast<float>(M.vmax);
+        const uint32_t ktop = KeyTraits<Raw>::kBits == 16 ? key_of(static_cast<uint16_t>(__float_as_uint(top) >> 16))
+                                                          : key_of(__float_as_uint(top));
+        const float vm = static_cast<float>(M.vmax + log(static_cast<double>(s.m)) / M.inv_t);
+        int b = max(kb_one(__float_as_uint(top) >> 16), kb_one(__float_as_uint(vm) >> 16) - 2);
+        for (; b < kKbBins; ++b) {
+          kb_keys<Raw>(b, klo, khi);
+          if (ONE && b == static_cast<int>(kKbSpan)) klo = khi = 0x7FFFu;
+          klo = min(klo, ktop);
+          khi = min(khi, ktop);
+          if (!(M.w(KeyTraits<Raw>::decode(klo)) >= static_cast<double>(s.m))) break;
+        }
+        if (b == kKbBins) continue;
+        const int at = (b & ~31) + lane;
+        const u64 c = sh.cnt[at];
+        const u64 m = c == 0ull ? 0ull : ONE ? sh.w[at] * c : (static_cast<u64>(sh.hi[at]) << 32) + sh.lo[at];
+        f.bin = b;
+        f.cnt = sh.run_cnt[b >> 5] + rs_warp_sum(at < b ? c : 0ull);
+        f.mass = sh.run_mass[b >> 5] + rs_warp_sum(at < b ? m : 0ull);
+        f.n = __shfl_sync(0xffffffffu, c, b & 31);
+        if (f.cnt >= n) continue;
+        if (ONE && d.middle && b == static_cast<int>(kKbSpan)) {
+          q.op = kRsLook;
+          break;
+        }
+        if (f.n == 0ull || ONE || !(M.w(KeyTraits<Raw>::decode(khi)) >= static_cast<double>(s.m))) {
+          n = f.cnt;
+          mass = f.mass;
+          continue;
+        }
+        asked = q.op = kRsSum;
+        q.klo = first_above<Raw>(M, s.m, klo, khi);
+        q.khi = khi;
+        break;
+      } else {
+        by_mass = true;
+        t = draw_target(s.u, mass);
+      }
+      f = kb_find<ONE>(sh, by_mass, t);
+      if (phase == 1 && f.cnt >= n) {  // not before the top-k cut
+        phase = 2;
+        continue;
+      }
+      if (ONE && d.middle && f.bin == static_cast<int>(kKbSpan)) {
+        q.op = kRsLook;
+        break;
+      }
+      kb_keys<Raw>(f.bin, klo, khi);
+      open = true;
+    }
+    if (!found) {  // inside the range
+      if (ONE || klo == khi) {
+        key = ONE && f.bin == static_cast<int>(kKbSpan) ? 0x7FFFu : khi;
+        const u64 w = ONE ? sh.w[f.bin] : M.fixed(KeyTraits<Raw>::decode(khi));
+        tie = by_mass ? (t - f.mass + w - 1) / w : t - f.cnt;
+        cnt = f.cnt + tie;
+        sum = f.mass + tie * w;
+      } else if (f.n == 1ull && phase < 3) {
+        cnt = f.cnt + 1ull;
+        sum = f.mass + f.m;
+      } else {
+        asked = q.op = f.n <= static_cast<u64>(kRsCap) ? kRsCollect : kRsZoom;
+        q.klo = klo;
+        q.khi = khi;
+        break;
+      }
+    }
+    // the cut's element is known
+    found = open = false;
+    if (phase == 3) {
+      q.op = tie ? kRsTies : kRsStop;
+      q.klo = key;
+      q.a = tie;
+      break;
+    }
+    if (cnt < n) {
+      n = cnt;
+      mass = sum;
+    }
+    ++phase;
+  }
+  if (lane == 0) {
+    d.phase = phase;
+    d.n = n;
+    d.mass = mass;
+    d.t = t;
+    d.by_mass = by_mass;
+    d.klo = klo;
+    d.khi = khi;
+    d.f = f;
+    d.asked = asked;
+    d.key = key;
+    d.id = id;
+    *out = q;
+  }
+  __syncwarp();
+}
+
+// The r-th token (from 1) of those with this key, into *token.
+template <typename Raw>
+__device__ __noinline__ void draw_tie(uint32_t key, u64 r, int32_t* token) {
+  rs_ties<Raw>(key, r - 1ull, r, [token](int id, u64) { *token = id; });
+}
+
+// The cuts and the draw from the row's bins (kb_chunks done).  False: a cut
+// fell into the zeros' bin, which may hold other values (`middle`).
+template <typename Raw, bool ONE>
+__device__ __forceinline__ bool draw_from_bins(const SampleParams& P, int row, const Settings& s, RsRow<Raw>& R,
+                                               bool middle) {
+  RsShared& sh = rs_shared();
+  if (R.rank == 0 && threadIdx.x == 0) {
+    RsDraw& d = sh.draw;
+    d.s = s;
+    d.phase = 0;
+    d.asked = kRsStop;
+    d.middle = middle;
+    d.n = sh.run_cnt[32 * kKbPerLane];
+    d.mass = sh.run_mass[32 * kKbPerLane];
+  }
+  __syncwarp();
+  for (;;) {
+    const RsMsg msg = R.broadcast([&](RsMsg* out) {
+      if (threadIdx.x < 32) draw_step<Raw, ONE>(out);
     });
-  if (lead) {
-    if (!h.tie) P.token[row] = h.id;
-    write_row(P, row, M.z(KeyTraits<Raw>::decode(h.key)), mass, n, M);
+    if constexpr (!ONE) {
+      if (msg.op == kRsCollect) {
+        cta_sync();
+        if (threadIdx.x == 0) sh.nlist = 0u;
+        R.sync();
+        const uint32_t k = min(rs_collect<Raw>(false, msg.klo, msg.khi), static_cast<uint32_t>(kRsCap));
+        if (R.rank == 0) {
+          rs_sort(k, k);
+          rs_list_masses<Raw>(sh, k);
+        }
+        continue;
+      }
+      if (msg.op == kRsZoom) {
+        int shift = 0;
+        while (((msg.khi - msg.klo) >> shift) >= static_cast<uint32_t>(kRsZoomBins)) ++shift;
+        rs_zoom<Raw>(msg.klo, msg.khi, shift);
+        continue;
+      }
+      if (msg.op == kRsSum) {
+        rs_sum<Raw>(msg.klo, msg.khi);
+        continue;
+      }
+    }
+    if (ONE && msg.op == kRsLook) return false;
+    if (R.rank == 0 && threadIdx.x == 0) {
+      const RsDraw& d = sh.draw;
+      if (msg.op == kRsStop) P.token[row] = d.id;
+      write_row(P, row, sh.M.z(KeyTraits<Raw>::decode(d.key)), d.mass, d.n, sh.M);
+    }
+    __syncwarp();
+    if (msg.op == kRsTies) draw_tie<Raw>(msg.klo, msg.a, P.token + row);
+    break;
   }
   R.sync();  // peers may still read this CTA's words
+  return true;
+}
+
+// Any row, any type, any setting.
+template <typename Raw>
+__device__ __forceinline__ void draw_general(const SampleParams& P, int row, const Settings& s, RsRow<Raw>& R,
+                                             uint32_t kmax) {
+  rs_set_masses(KeyTraits<Raw>::decode(kmax), s.t, P.fx_shift);
+  kb_masses<Raw>();
+  if (R.rank == 0) kb_chunks<Raw, false>();
+  draw_from_bins<Raw, false>(P, row, s, R, false);
+}
+
+// A bf16 row from the counts of its values: one pass over the row (one shared
+// atomic per element and no exponential), and a second one from L2 that finds
+// the drawn token among those of its value.  Returns false when the row needs
+// the general path: values beyond the bins' range that matter.
+__device__ __forceinline__ bool draw_by_value(const SampleParams& P, int row, const Settings& s, RsRow<uint16_t>& R) {
+  RsShared& sh = rs_shared();
+  cta_sync();  // the geometry
+  kb_count<uint16_t>();
+  const RsMsg ends = R.broadcast([&](RsMsg* m) {
+    if (threadIdx.x == 0) {
+      m->flag = sh.cnt[0];
+      m->klo = sh.cnt[kKbSpan];
+      m->khi = sh.cnt[kKbBins - 1];
+      sh.first = kKbBins;
+    }
+  });
+  if (ends.flag) return false;  // above 2^17, +inf or NaN
+  uint32_t low = ends.khi;      // unmasked values of the last bin
+  {
+    u64 masked = 0ull, nan = 0ull;
+    for (int c = 0; low && c < R.C; ++c) {
+      masked += R.peer(sh.y, c)[0];
+      nan |= R.peer(sh.y, c)[1];
+    }
+    if (nan) return false;
+    low -= static_cast<uint32_t>(masked);
+  }
+  bool middle = ends.klo != 0u;
+  const RsMsg got = R.broadcast([&](RsMsg* msg) {
+    if (threadIdx.x == 0) sh.cnt[kKbBins - 1] = low;
+    cta_sync();
+    int first = kKbBins;
+#pragma unroll 4
+    for (int b = kKbAll - kRsThreads + static_cast<int>(threadIdx.x); b >= 0; b -= kRsThreads)
+      if (b < kKbBins && sh.cnt[b]) first = b;
+    first = static_cast<int>(__reduce_min_sync(0xffffffffu, static_cast<uint32_t>(first)));
+    if ((threadIdx.x & 31) == 0 && first < kKbBins) atomicMin(&sh.first, static_cast<uint32_t>(first));
+    cta_sync();
+    first = static_cast<int>(sh.first);
+    uint32_t flag = 0u;
+    if (first >= kKbBins) {
+      flag = 2u;  // every token masked
+    } else {
+      uint32_t klo, khi;
+      kb_keys<uint16_t>(first, klo, khi);
+      if (first == static_cast<int>(kKbSpan)) khi = 0x7FFFu;
+      rs_set_masses(KeyTraits<uint16_t>::decode(khi), s.t, P.fx_shift);
+      cta_sync();
+      if (low && sh.M.z(-131072.f) >= -46.0) flag = 1u;  // the last bin's values have masses of their own
+      if (!flag) kb_chunks<uint16_t, true>();
+    }
+    if (threadIdx.x == 0) {
+      // the zeros' bin is taken as zeros as long as no cut falls into it and its mass, off by
+      // at most 2^-24 / T of itself, moves the row's sum by less than 2^-40
+      if (!flag && middle && static_cast<double>(sh.w[kKbSpan]) * sh.cnt[kKbSpan] * 65536.0 * sh.M.inv_t >
+                                 static_cast<double>(sh.run_mass[32 * kKbPerLane]))
+        flag = 3u;
+      msg->flag = flag;
+    }
+  });
+  if (got.flag == 1u) return false;
+  if (got.flag == 3u) {
+    if (kb_tiny()) return false;
+    middle = false;
+  }
+  if (got.flag == 2u) {
+    if (R.rank == 0 && threadIdx.x == 0) write_none(P, row, VS_ROW_EMPTY_SUPPORT);
+    R.sync();
+    return true;
+  }
+  while (!draw_from_bins<uint16_t, true>(P, row, s, R, middle)) {
+    if (kb_tiny()) return false;
+    middle = false;
+  }
+  return true;
+}
+
+template <typename Raw>
+__global__ void __launch_bounds__(kRsThreads, 1) sample_kernel(SampleParams P) {
+  RsRow<Raw> R;
+  const int row = static_cast<int>(blockIdx.x / cg::this_cluster().num_blocks());
+  R.init(P.logits, row, P.ld, P.vocab);
+  const bool lead = R.rank == 0 && threadIdx.x == 0;
+
+  Settings s;
+  s.t = P.temperature ? P.temperature[row] : P.temperature_scalar;
+  s.k = P.top_k ? P.top_k[row] : P.top_k_scalar;
+  s.p = P.top_p ? P.top_p[row] : P.top_p_scalar;
+  s.m = P.min_p ? P.min_p[row] : P.min_p_scalar;
+  s.u = P.uniform[row];
+  const bool fine = s.t >= 0.f && s.t < kInf && s.p > 0.f && s.m <= 1.f && s.u >= 0.f && s.u <= 1.f;
+  if (fine && s.t == 0.f) {  // greedy: the first token of the order
+    s.t = 1.f;
+    s.k = 1;
+    s.p = 1.f;
+    s.m = 0.f;
+  }
+  const bool listed = s.k > 0 && s.k < P.vocab && s.k <= kListTopK;
+  bool by_value = sizeof(Raw) == 2 && fine && !listed, by_list = listed;
+  for (;;) {
+    if constexpr (sizeof(Raw) == 2) {
+      if (by_value && draw_by_value(P, row, s, R)) return;
+    }
+    cta_sync();  // the geometry
+    const uint32_t kmax = rs_max<Raw>();
+    const bool finite = kmax < KeyTraits<Raw>::kInfKey;
+    const bool empty = finite && kmax <= RsRow<Raw>::kMaskedKey;
+    if (!finite || !fine || empty) {
+      if (lead)
+        write_none(P, row, (finite ? 0u : VS_ROW_NONFINITE_INPUT) | (fine ? 0u : VS_ROW_BAD_PARAM) |
+                               (empty ? VS_ROW_EMPTY_SUPPORT : 0u));
+      R.sync();  // peers read this CTA's maximum
+      return;
+    }
+    if (by_list) {
+      rs_set_masses(KeyTraits<Raw>::decode(kmax), s.t, P.fx_shift);
+      const uint32_t floor_key = max(rs_topk_floor<Raw>(s.k), RsRow<Raw>::kMaskedKey + 1u);
+      const uint32_t n_list = rs_collect<Raw>(true, floor_key, kmax);
+      if (n_list <= static_cast<uint32_t>(kRsCap)) {
+        if (R.rank == 0) draw_from_list<Raw>(P, row, s, n_list);
+        return;  // rs_collect ended with a cluster barrier: nothing is read from peers after it
+      }
+      by_list = false;
+      by_value = sizeof(Raw) == 2;
+      if (by_value) continue;
+    }
+    draw_general(P, row, s, R, kmax);
+    return;
+  }
 }
 
 }  // namespace
@@ -216,29 +517,88 @@ cudaError_t launch_sample(const SampleParams& P, vs_dtype dtype, cudaStream_t s)
 
 namespace {
 
+// More elements than a list holds lie above the floor: the k-th element's bin
+// from counts, zoomed into until the bins down to it fit the list, or until
+// it is one value, whose first tokens complete those above it.  Returns the
+// list's length.
+template <typename Raw>
+__device__ __forceinline__ uint32_t topk_general(const TopkParams& P, RsRow<Raw>& R, float vmax, float t,
+                                                 uint32_t kmax) {
+  RsShared& sh = rs_shared();
+  rs_set_masses(vmax, t, P.fx_shift);
+  kb_count<Raw>();
+  if (R.rank == 0) kb_chunks<Raw, true>();
+  const u64 k = static_cast<u64>(P.k);
+  RsBin f{0, 0ull, 0ull, 0ull, 0ull};
+  uint32_t klo = 0u, khi = 0u;
+  bool zoomed = false;
+  for (;;) {
+    const RsMsg msg = R.broadcast([&](RsMsg* out) {
+      if (threadIdx.x >= 32) return;
+      if (!zoomed) {
+        f = kb_find<true>(sh, false, k);
+        kb_keys<Raw>(f.bin, klo, khi);
+      } else {
+        int shift = 0;
+        while (((khi - klo) >> shift) >= static_cast<uint32_t>(kRsZoomBins)) ++shift;
+        f = rs_find_zoom(sh, false, k, f.cnt, f.mass);
+        const uint32_t top = khi - (static_cast<uint32_t>(f.bin) << shift), width = (1u << shift) - 1u;
+        klo = top - klo > width ? top - width : klo;
+        khi = top;
+      }
+      if (threadIdx.x == 0) {
+        out->op = f.cnt + f.n <= static_cast<u64>(kRsCap) ? kRsCollect : klo == khi ? kRsTies : kRsZoom;
+        out->klo = klo;
+        out->khi = khi;
+        out->a = f.cnt;
+      }
+    });
+    zoomed = true;
+    if (msg.op == kRsZoom) {
+      int shift = 0;
+      while (((msg.khi - msg.klo) >> shift) >= static_cast<uint32_t>(kRsZoomBins)) ++shift;
+      rs_zoom<Raw>(msg.klo, msg.khi, shift);
+      continue;
+    }
+    cta_sync();
+    if (threadIdx.x == 0) sh.nlist = 0u;
+    R.sync();
+    if (msg.op == kRsCollect) {
+      return rs_collect<Raw>(false, msg.klo, kmax);
+    }
+    const uint32_t above = msg.klo < kmax ? rs_collect<Raw>(false, msg.klo + 1u, kmax) : 0u;
+    u64* list = R.peer(sh.list, 0);
+    rs_ties<Raw>(msg.klo, 0ull, k - min(k, static_cast<u64>(above)), [=](int id, u64 at) {
+      list[above + at] = (static_cast<u64>(msg.klo) << 32) | static_cast<uint32_t>(~id);
+    });
+    R.sync();
+    return static_cast<uint32_t>(P.k);
+  }
+}
+
 // vs_topk_logprob: the first k tokens of each row in the total order and
 // their log-probabilities  z_j - log sum_i exp z_i,  z = l / T.
 template <typename Raw>
 __global__ void __launch_bounds__(kRsThreads, 1) topk_kernel(TopkParams P) {
-  extern __shared__ __align__(16) unsigned char rs_smem[];
-  RsShared& sh = *reinterpret_cast<RsShared*>(rs_smem);
+  RsShared& sh = rs_shared();
   RsRow<Raw> R;
   const int row = static_cast<int>(blockIdx.x / cg::this_cluster().num_blocks());
-  R.init(P.logits, row, P.ld, P.vocab, &sh);
+  R.init(P.logits, row, P.ld, P.vocab);
   int32_t* ids = P.ids + static_cast<int64_t>(row) * P.out_ld;
   float* lps = P.logprob ? P.logprob + static_cast<int64_t>(row) * P.out_ld : nullptr;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const float t = P.temperature ? P.temperature[row] : P.temperature_scalar;
   const bool fine = t > 0.f && t < kInf;
 
-  uint32_t kmax, kmin, thread_max;
-  const bool finite = rs_extremes(R, kmax, kmin, thread_max);
+  cta_sync();  // the geometry
+  const uint32_t kmax = rs_max<Raw>();
+  const bool finite = kmax < KeyTraits<Raw>::kInfKey;
   const bool empty = finite && kmax <= RsRow<Raw>::kMaskedKey;
   if (!finite || !fine || empty) {
     if (R.rank == 0) {
-      if (tid < P.k) {
-        ids[tid] = -1;
-        if (lps) lps[tid] = empty && fine ? -kInf : __int_as_float(0x7FC00000);
+      for (int i = tid; i < P.k; i += kRsThreads) {
+        ids[i] = -1;
+        if (lps) lps[i] = empty && fine ? -kInf : __int_as_float(0x7FC00000);
       }
       if (tid == 0 && P.status)
         P.status[row] = (finite ? 0u : VS_ROW_NONFINITE_INPUT) | (fine ? 0u : VS_ROW_BAD_PARAM) |
@@ -263,7 +623,7 @@ __global__ void __launch_bounds__(kRsThreads, 1) topk_kernel(TopkParams P) {
     if (lane == 0) sh.fred[warp] = z;
     cta_sync();
     if (warp == 0) {
-      z = sh.fred[lane];
+      z = lane < kRsWarps ? sh.fred[lane] : 0.f;
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
       if (lane == 0) sh.xf[0] = z;
@@ -271,41 +631,21 @@ __global__ void __launch_bounds__(kRsThreads, 1) topk_kernel(TopkParams P) {
   }
 
   uint32_t n = 0u, nk = 0u;
-  const uint32_t floor_key = max(rs_topk_floor(R, thread_max, P.k), RsRow<Raw>::kMaskedKey + 1u);
-  n = rs_collect(R, floor_key, kmax);
-  if (n > static_cast<uint32_t>(kRsCap)) {
-    // too many elements share the floor: the k-th element exactly, then the
-    // elements above it and its first equals
-    RsMass M;
-    M.vmax = static_cast<double>(vmax);
-    M.inv_t = 1.0 / static_cast<double>(t);
-    M.scale = static_cast<double>(1ull << P.fx_shift);
-    RsBins B;
-    B.vmax = vmax;
-    const float range = B.vmax - KeyTraits<Raw>::decode(kmin);
-    B.s = range > 0.f ? fminf(static_cast<float>(kRsBins - 1) / range, 1e38f) : 0.f;
-    rs_hist(R, M, kRsBins, sh.rcnt, sh.rmass, [&](uint32_t, float v) { return B.of(v); });
-    const RsHit h = rs_find(R, M, B, kmin, kmax, false, static_cast<u64>(P.k));
-    n = h.key < kmax ? rs_collect(R, h.key + 1u, kmax) : 0u;
-    u64* list = R.peer(sh.list, 0);
-    rs_ties(R, h.key, static_cast<u64>(P.k) - n, [&](int id, u64 at) {
-      list[n + at] = (static_cast<u64>(h.key) << 32) | static_cast<uint32_t>(~id);
-    });
-    n = static_cast<uint32_t>(P.k);
-    R.sync();
-  }
+  const uint32_t floor_key = max(rs_topk_floor<Raw>(P.k), RsRow<Raw>::kMaskedKey + 1u);
+  n = rs_collect<Raw>(true, floor_key, kmax);
+  if (n > static_cast<uint32_t>(kRsCap)) n = topk_general(P, R, vmax, t, kmax);
   nk = min(static_cast<uint32_t>(P.k), n);
   if (R.rank == 0) {
     float z = 0.f;
     if (lps)
       for (int r = 0; r < R.C; ++r) z += R.peer(sh.xf, r)[0];
-    rs_sort(sh, n, nk);
-    if (tid < P.k) {
-      const bool in = static_cast<uint32_t>(tid) < nk;
-      const u64 e = in ? sh.sorted[tid] : 0ull;
-      ids[tid] = in ? static_cast<int32_t>(~static_cast<uint32_t>(e)) : -1;
+    rs_sort(n, nk);
+    for (int i = tid; i < P.k; i += kRsThreads) {
+      const bool in = static_cast<uint32_t>(i) < nk;
+      const u64 e = in ? sh.sorted[i] : 0ull;
+      ids[i] = in ? static_cast<int32_t>(~static_cast<uint32_t>(e)) : -1;
       if (lps)
-        lps[tid] = in ? (KeyTraits<Raw>::decode(static_cast<uint32_t>(e >> 32)) - vmax) / t - logf(z) : -kInf;
+        lps[i] = in ? (KeyTraits<Raw>::decode(static_cast<uint32_t>(e >> 32)) - vmax) / t - logf(z) : -kInf;
     }
     if (tid == 0 && P.status) P.status[row] = 0u;
   }
