@@ -485,7 +485,7 @@ vs_status check_rows(int32_t rows, int32_t vocab, int64_t ld, vs_dtype dtype, co
   if (dtype != VS_F32 && dtype != VS_BF16)
     return fail(VS_ERR_INVALID_ARG, "dtype must be VS_BF16 or VS_F32");
   if (rows == 0) return VS_OK;
-  if (rows > (1 << 27)) return fail(VS_ERR_UNSUPPORTED, "rows must be at most 2^27");
+  if (rows > (1 << 24)) return fail(VS_ERR_UNSUPPORTED, "rows must be at most 2^24");
   if (!logits || !aligned16(logits))
     return fail(VS_ERR_INVALID_ARG, "logits must be non-NULL and 16-byte aligned");
   if ((static_cast<uint64_t>(ld) * esize(dtype)) % 16 != 0)

@@ -36,13 +36,15 @@ constexpr int kBThreads = 256;  // backward kernel
 struct alignas(16) DistillCtx {
   float c;      // log2(e) / T
   float inv_t;  // 1 / T
-  float ref;    // log2 normaliser of the dense part (the row's, or that outside the list)
-  float coef;   // factor of the dense part: 1, or q_t - a_t
-  float lse2;   // log2 sum_j 2^(l_j c)
-  float tnorm;  // teacher: a_k = exp(lp_k - tnorm)
-  uint32_t zero;  // no gradient (empty list, non-finite row)
-  uint32_t dup;   // the list repeats an id
-  uint32_t pad[8];
+  // an element's share is 2^((l - ref) c - lz): the differences of the logits come first, so that
+  // l c may overflow (rows at the type's lowest value)
+  float ref, lz;    // of the dense part: the whole row's, or what lies outside the list
+  float coef;       // factor of the dense part: 1, or q_t - a_t
+  float rall, lall; // the whole row's
+  float tnorm;      // teacher: a_k = exp(lp_k - tnorm)
+  uint32_t zero;    // no gradient (empty list, non-finite row)
+  uint32_t dup;     // the list repeats an id
+  uint32_t pad[6];
 };
 static_assert(sizeof(DistillCtx) == VS_CTX_BYTES_PER_ROW, "ctx layout");
 
@@ -108,14 +110,14 @@ __device__ __forceinline__ void grad_pass(const Raw* __restrict__ row, G* __rest
       if constexpr (ACC) o.load(out + j);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        float d = k.zero ? 0.f : dense * ex2(fmaf(value_of(x.e[i]), k.c, -k.ref));
+        float d = k.zero ? 0.f : dense * ex2(fmaf(value_of(x.e[i]) - k.ref, k.c, -k.lz));
         if constexpr (ACC) d += grad_value(o.e[i]);
         o.e[i] = to_grad<G>(d);
       }
       o.store(out + j);
     } else {
       for (int i = j; i < j1; ++i) {
-        float d = k.zero ? 0.f : dense * ex2(fmaf(value_of(row[i]), k.c, -k.ref));
+        float d = k.zero ? 0.f : dense * ex2(fmaf(value_of(row[i]) - k.ref, k.c, -k.lz));
         if constexpr (ACC) d += grad_value(out[i]);
         out[i] = to_grad<G>(d);
       }
@@ -128,7 +130,7 @@ __device__ __forceinline__ void grad_pass(const Raw* __restrict__ row, G* __rest
     const int s = threadIdx.x + i * NT;
     const int id = s < width ? ids[s] : -1;
     if (id >= j0 && id < j1 && (!k.dup || first_of(ids, s))) {
-      const float q = ex2(fmaf(value_of(row[id]), k.c, -k.lse2));
+      const float q = ex2(fmaf(value_of(row[id]) - k.rall, k.c, -k.lall));
       float d = scale * (q - expf(lp[s] - k.tnorm));
       if constexpr (ACC) d += old[i];
       out[id] = to_grad<G>(d);
@@ -174,9 +176,9 @@ struct alignas(16) DistillShared {
   uint32_t status, dup;
 };
 
-// Online sum of 2^(l c - m) over a thread's elements.
+// Online sum of 2^((l - v) c) over a thread's elements.
 struct Online {
-  float v, m, z;  // largest logit, m = fl(v c), the sum
+  float v, z;  // largest logit, the sum
   uint32_t bad;
   template <typename Raw>
   __device__ __forceinline__ void add(const Raw (&r)[8], uint32_t listed, float c) {
@@ -192,10 +194,8 @@ struct Online {
 #pragma unroll
     for (int i = 1; i < 8; ++i) t = fmaxf(t, x[i]);
     if (t > v) {
-      const float mn = __fmul_rn(t, c);
-      z = v == -kInf ? 0.f : z * ex2(m - mn);
+      z = v == -kInf ? 0.f : z * ex2((v - t) * c);
       v = t;
-      m = mn;
     }
     if (v == -kInf) {  // nothing but masked elements so far, or NaN
 #pragma unroll
@@ -204,7 +204,7 @@ struct Online {
     }
     float s = 0.f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) s += ex2(fmaf(x[i], c, -m));
+    for (int i = 0; i < 8; ++i) s += ex2((x[i] - v) * c);
     z += s;
   }
 };
@@ -264,7 +264,7 @@ __global__ void __launch_bounds__(kDThreads) distill_fwd_kernel(DistillParams P)
   }
 
   // the slice outside the list
-  Online o{-kInf, -kInf, 0.f, 0u};
+  Online o{-kInf, 0.f, 0u};
   for (int j = j0 + tid * 8; j < j1; j += kDThreads * 8) {
     Eight<Raw> q;
     if (j + 8 <= j1)
@@ -279,7 +279,7 @@ __global__ void __launch_bounds__(kDThreads) distill_fwd_kernel(DistillParams P)
   constexpr int SLOTS = (VS_MAX_SUPPORT_WIDTH + kDThreads - 1) / kDThreads;
   double lp[SLOTS], u[SLOTS];
   bool kept[SLOTS];
-  Three mx{-kInf, -kInf, o.m};
+  Three mx{-kInf, -kInf, o.v};
   uint32_t bad = o.bad || !(o.z < kInf) ? 1u : 0u;  // this slice, and the list
   uint32_t any = 0u;
 #pragma unroll
@@ -292,7 +292,7 @@ __global__ void __launch_bounds__(kDThreads) distill_fwd_kernel(DistillParams P)
       const float v = value_of(x[id]), l = sh.lp[s];
       bad |= !(v < kInf) || !(l < kInf) ? 1u : 0u;
       lp[i] = static_cast<double>(l);
-      u[i] = static_cast<double>(v) * static_cast<double>(c);
+      u[i] = static_cast<double>(v);
       mx.a = fmax(mx.a, lp[i]);
       mx.b = fmax(mx.b, u[i]);
       any = 1u;
@@ -301,12 +301,13 @@ __global__ void __launch_bounds__(kDThreads) distill_fwd_kernel(DistillParams P)
   mx = block_three<true>(mx, sh.red);
   const bool tail = P.tail != 0;
   const double toff = tail ? 0.0 : mx.a;
-  Three sum{0.0, 0.0, o.z == 0.f ? 0.0 : static_cast<double>(o.z) * exp2(static_cast<double>(o.m) - mx.c)};
+  const double cd = static_cast<double>(c);  // the same factor everywhere: its rounding cancels
+  Three sum{0.0, 0.0, o.z == 0.f ? 0.0 : static_cast<double>(o.z) * exp2((static_cast<double>(o.v) - mx.c) * cd)};
 #pragma unroll
   for (int i = 0; i < SLOTS; ++i)
     if (kept[i]) {
       sum.a += lp[i] == -kInf ? 0.0 : exp(lp[i] - toff);
-      sum.b += u[i] == -kInf ? 0.0 : exp2(u[i] - mx.b);
+      sum.b += u[i] == -kInf ? 0.0 : exp2((u[i] - mx.b) * cd);
     }
   sum = block_three<false>(sum, sh.red);
   __syncwarp();
@@ -329,17 +330,16 @@ __global__ void __launch_bounds__(kDThreads) distill_fwd_kernel(DistillParams P)
     for (int r = 0; r < C; ++r) mr = fmax(mr, cl.map_shared_rank(sh.part, r)[0]);
     for (int r = 0; r < C; ++r) {
       const double* p = cl.map_shared_rank(sh.part, r);
-      if (p[1] != 0.0) zr += p[1] * exp2(p[0] - mr);
+      if (p[1] != 0.0) zr += p[1] * exp2((p[0] - mr) * cd);
       bad |= *cl.map_shared_rank(&sh.part_bad, r);
     }
   }
   const double m = fmax(mr, mx.b);
-  const double z = (zr != 0.0 ? zr * exp2(mr - m) : 0.0) + (sum.b != 0.0 ? sum.b * exp2(mx.b - m) : 0.0);
+  const double z = (zr != 0.0 ? zr * exp2((mr - m) * cd) : 0.0) + (sum.b != 0.0 ? sum.b * exp2((mx.b - m) * cd) : 0.0);
   if (!(z > 0.0)) bad = 1u;  // every logit masked, or NaN
-  const double lse2 = m + log2(z);
-  const double lr2 = zr > 0.0 ? mr + log2(zr) : -kInf;
+  const double lz = log2(z), lr = zr > 0.0 ? (mr - m) * cd + log2(zr) - lz : -kInf;  // log2 q_t
   const double at = tail ? fmax(0.0, 1.0 - sum.a) : 0.0;
-  const double qt = zr > 0.0 ? exp2(lr2 - lse2) : 0.0;
+  const double qt = zr > 0.0 ? exp2(lr) : 0.0;
   const bool empty = any == 0u || (!tail && !(sum.a > 0.0));
   const double tnorm = tail ? 0.0 : toff + log(sum.a);
   const bool live = fine && !bad && !empty;
@@ -350,19 +350,21 @@ __global__ void __launch_bounds__(kDThreads) distill_fwd_kernel(DistillParams P)
   for (int i = 0; i < SLOTS; ++i)
     if (kept[i] && live) {
       const double l = lp[i] - tnorm, a = exp(l);
-      if (a > 0.0) loss += a * (l - kLn2d * (u[i] - lse2));
+      if (a > 0.0) loss += a * (l - kLn2d * ((u[i] - m) * cd - lz));
     }
   Three fin = block_three<false>(Three{loss, 0.0, 0.0}, sh.red);
   loss = fin.a;
-  if (live && at > 0.0 && zr > 0.0) loss += at * (log(at) - kLn2d * (lr2 - lse2));
+  if (live && at > 0.0 && zr > 0.0) loss += at * (log(at) - kLn2d * lr);
 
   DistillCtx k{};
   k.c = c;
   k.inv_t = 1.f / t;
   const bool outside = tail && zr > 0.0;
-  k.ref = static_cast<float>(outside ? lr2 : lse2);
+  k.rall = static_cast<float>(m);
+  k.lall = static_cast<float>(lz);
+  k.ref = outside ? static_cast<float>(mr) : k.rall;
+  k.lz = outside ? static_cast<float>(log2(zr)) : k.lall;
   k.coef = tail ? (outside ? static_cast<float>(qt - at) : 0.f) : 1.f;
-  k.lse2 = static_cast<float>(lse2);
   k.tnorm = static_cast<float>(tnorm);
   k.zero = live ? 0u : 1u;
   k.dup = sh.dup;
@@ -385,6 +387,391 @@ __global__ void __launch_bounds__(kDThreads) distill_fwd_kernel(DistillParams P)
   }
 }
 
+// ---------------------------------------------------------------------------
+// Rows whose slices fit shared memory: every CTA of the cluster copies its
+// slice there once (a bulk asynchronous copy), and all passes read that copy,
+// so a call reads each logit from HBM once and, with a gradient, writes it
+// once.  The listed elements are taken out of the copy (set to -inf) before
+// the sums.  Warp 0 goes through the teacher's list in fp64 while the other
+// warps go through the slice; the CTAs' parts are pushed into the shared
+// memory of those that need them (the leader's, with a gradient everyone's).
+// A CTA holds its shared memory for a few microseconds of mostly latency, so
+// the rate is that of the slots: 40 KB slices, five CTAs per SM.
+
+constexpr int kSThreads = 256;
+constexpr int kSWarps = kSThreads / 32;
+constexpr int kSSlice = kSThreads - 32;  // threads of the slice passes
+constexpr int kSMaxCluster = 8;
+
+// One CTA's part of the row's sums of 2^((l - m) c): 48 bytes.
+struct alignas(16) DistillPart {
+  float mr, zr;  // outside the list: largest logit, and the sum below it
+  float ml, zl;  // its listed elements
+  double w, wu;  // sums of the teacher's weight, and of it times (l - ml) c, over its listed elements
+  uint32_t bad, pad[3];
+};
+
+struct alignas(16) DistillStage {
+  DistillPart parts[kSMaxCluster];  // from the CTA of each rank
+  DistillCtx k;
+  uint64_t bar, xbar;  // the slice's copy; the parts
+  double s0, t1, tnorm, at;
+  float2 red[kSWarps];
+  uint32_t status, dup, any, bad;
+};
+
+// Room behind it: the list's ids, teacher values and student values, and a
+// hash table of at least twice its width; then the slice.
+__host__ __device__ inline int stage_width(int width) { return (width + 3) / 4 * 4; }
+__host__ __device__ inline int stage_hash(int width) {
+  int h = 64;
+  while (h < 2 * width) h *= 2;
+  return h;
+}
+__host__ __device__ inline size_t stage_fixed(int width) {
+  return sizeof(DistillStage) + 12 * static_cast<size_t>(stage_width(width)) + 4 * static_cast<size_t>(stage_hash(width));
+}
+
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
+// Largest of eight elements (NaN if there is one).
+__device__ __forceinline__ float max8(const Eight<uint16_t>& v) {
+  uint32_t m = 0xFF80FF80u;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t w = reinterpret_cast<const uint32_t*>(v.q)[i];
+    const __nv_bfloat162 r = __hmax2_nan(*reinterpret_cast<const __nv_bfloat162*>(&m),
+                                         *reinterpret_cast<const __nv_bfloat162*>(&w));
+    m = *reinterpret_cast<const uint32_t*>(&r);
+  }
+  return max_nan(__uint_as_float(m << 16), __uint_as_float(m & 0xFFFF0000u));
+}
+__device__ __forceinline__ float max8(const Eight<uint32_t>& v) {
+  float m = __uint_as_float(v.e[0]);
+#pragma unroll
+  for (int i = 1; i < 8; ++i) m = max_nan(m, __uint_as_float(v.e[i]));
+  return m;
+}
+__device__ __forceinline__ f32x2 pair_of(const Eight<uint16_t>& v, int i) {
+  const uint32_t w = reinterpret_cast<const uint32_t*>(v.q)[i];
+  return pack2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+}
+__device__ __forceinline__ f32x2 pair_of(const Eight<uint32_t>& v, int i) {
+  return pack2(__uint_as_float(v.e[2 * i]), __uint_as_float(v.e[2 * i + 1]));
+}
+
+template <typename T>
+__device__ __forceinline__ T warp_sum(T x) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+  return x;
+}
+__device__ __forceinline__ float warp_max_nan(float x) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) x = max_nan(x, __shfl_xor_sync(0xffffffffu, x, o));
+  return x;
+}
+
+// A part into a peer's shared memory, counted on its barrier.
+__device__ __forceinline__ uint32_t peer_addr(const void* p, uint32_t rank) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(smem_addr(p)), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ void push_part(uint32_t dst, uint32_t bar, const DistillPart& p) {
+  const uint32_t* w = reinterpret_cast<const uint32_t*>(&p);
+#pragma unroll
+  for (int i = 0; i < 3; ++i)
+    asm volatile(
+        "st.async.shared::cluster.mbarrier::complete_tx::bytes.v4.b32 [%0], {%2, %3, %4, %5}, [%1];" ::"r"(dst + 16u * i),
+        "r"(bar), "r"(w[4 * i]), "r"(w[4 * i + 1]), "r"(w[4 * i + 2]), "r"(w[4 * i + 3])
+        : "memory");
+}
+
+template <typename Raw, typename G, bool GRAD>
+__global__ void __launch_bounds__(kSThreads, 5) distill_stage_kernel(DistillParams P) {
+  extern __shared__ __align__(16) unsigned char d_smem[];
+  DistillStage& sh = *reinterpret_cast<DistillStage*>(d_smem);
+  const int W = P.width, W4 = stage_width(W), hsize = stage_hash(W);
+  int32_t* ids = reinterpret_cast<int32_t*>(d_smem + sizeof(DistillStage));  // -1: pad, bad or repeated
+  float* lps = reinterpret_cast<float*>(ids + W4);
+  float* us = lps + W4;
+  int32_t* hash = reinterpret_cast<int32_t*>(us + W4);
+  Raw* buf = reinterpret_cast<Raw*>(hash + hsize);
+  constexpr Raw kMasked = static_cast<Raw>(sizeof(Raw) == 2 ? 0xFF80u : 0xFF800000u);
+  cg::cluster_group cl = cg::this_cluster();
+  const int C = static_cast<int>(cl.num_blocks()), rank = static_cast<int>(cl.block_rank());
+  const int row = static_cast<int>(blockIdx.x) / C;
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int V = P.vocab;
+  const Raw* x = static_cast<const Raw*>(P.logits) + static_cast<int64_t>(row) * P.ld;
+  const int j0 = min(V, rank * P.chunk), j1 = min(V, j0 + P.chunk);
+  const int n = j1 - j0, groups = (n + 7) / 8;  // of eight elements, the last one filled up with masked ones
+  const uint32_t bytes = static_cast<uint32_t>(n / 8) * 8u * sizeof(Raw);
+
+  if (tid == 0) {
+    mbar_init(&sh.bar, 1);
+    mbar_init(&sh.xbar, 1);
+    fence_barrier_init();
+    fence_proxy_async();
+    if (GRAD || rank == 0) mbar_arrive_expect_tx(&sh.xbar, static_cast<uint32_t>(C * sizeof(DistillPart)));
+    if (bytes) {
+      mbar_arrive_expect_tx(&sh.bar, bytes);
+      bulk_load_all(buf, x + j0, bytes, &sh.bar);
+    }
+    sh.status = sh.dup = sh.any = sh.bad = 0u;
+  }
+  // the parts' barriers are ready everywhere once every CTA has arrived here
+  __syncwarp();
+  asm volatile("barrier.cluster.arrive.aligned;" ::: "memory");
+  const float t = P.temperature ? P.temperature[row] : P.temperature_scalar;
+  const bool fine = t > 0.f && t < kInf;
+  const float c = fminf(kLog2e / t, 3e38f);
+  const bool tail = P.tail != 0;
+  for (int i = n / 8 * 8 + tid; i < groups * 8; i += kSThreads) buf[i] = i < n ? x[j0 + i] : kMasked;
+
+  // the list, and whether it repeats an id
+  for (int i = tid; i < hsize / 4; i += kSThreads) reinterpret_cast<int4*>(hash)[i] = make_int4(-1, -1, -1, -1);
+  cta_sync();
+  for (int s = tid; s < W; s += kSThreads) {
+    const int64_t at = static_cast<int64_t>(row) * P.teacher_ld + s;
+    int32_t id = P.ids[at];
+    lps[s] = P.lp[at];
+    if (id < -1 || id >= V) {
+      atomicOr(&sh.status, VS_ROW_BAD_SUPPORT_ID);
+      id = -1;
+    }
+    ids[s] = id;
+    if (id >= 0) {
+      sh.any = 1u;
+      uint32_t h = (static_cast<uint32_t>(id) * 2654435761u) >> 16 & (hsize - 1);
+      for (int probe = 0; probe < hsize; ++probe) {  // at most half full: ends at a free place
+        const int32_t old = atomicCAS(&hash[h], -1, id);
+        if (old == -1) break;
+        if (old == id) {
+          sh.dup = 1u;
+          break;
+        }
+        h = (h + 1) & (hsize - 1);
+      }
+    }
+  }
+  cta_sync();
+  if (sh.dup) {
+    constexpr int kSlots = (VS_MAX_SUPPORT_WIDTH + kSThreads - 1) / kSThreads;
+    uint32_t drop = 0u;
+    for (int i = 0; i < kSlots; ++i) {
+      const int s = tid + i * kSThreads;
+      if (s < W && ids[s] >= 0 && !first_of(ids, s)) drop |= 1u << i;
+    }
+    cta_sync();
+    for (int i = 0; i < kSlots; ++i)
+      if (drop >> i & 1u) ids[tid + i * kSThreads] = -1;
+    cta_sync();
+  }
+
+  // take this slice's listed elements out of the copy
+  if (bytes && !mbar_wait(&sh.bar, 0)) atomicOr(&sh.bad, 2u);
+  __syncwarp();
+  for (int s = tid; s < W; s += kSThreads) {
+    const int id = ids[s];
+    const bool own = id >= j0 && id < j1;
+    us[s] = own ? value_of(buf[id - j0]) : -kInf;
+  }
+  cta_sync();  // a repeated id's slots are gone, so no two slots name one element
+  for (int s = tid; s < W; s += kSThreads) {
+    const int id = ids[s];
+    if (id >= j0 && id < j1) buf[id - j0] = kMasked;
+  }
+  cta_sync();
+
+  DistillPart mine{-kInf, 0.f, -kInf, 0.f, 0.0, 0.0, 0u, {0u, 0u, 0u}};
+  if (tid < 32) {
+    // the list: the teacher's sums s0 = sum w, t1 = sum w lp with w = exp(lp - off) over all of it, and the
+    // student's over this slice's elements
+    float off = -kInf;
+    if (!tail)
+      for (int s = lane; s < W; s += 32)
+        if (ids[s] >= 0) off = fmaxf(off, lps[s]);
+    off = tail ? 0.f : warp_max_nan(off);
+    if (!(off > -kInf)) off = 0.f;
+    float lmax = -kInf;
+    for (int s = lane; s < W; s += 32)
+      if (ids[s] >= j0 && ids[s] < j1) lmax = max_nan(lmax, us[s]);
+    lmax = warp_max_nan(lmax);
+    double s0 = 0.0, t1 = 0.0, ws = 0.0, wu = 0.0;
+    uint32_t bad = lmax < kInf ? 0u : 1u;  // NaN or +inf
+    float zl = 0.f;
+    for (int s = lane; s < W; s += 32) {
+      const int id = ids[s];
+      if (id < 0) continue;
+      const float l = lps[s], u = us[s];
+      const bool own = id >= j0 && id < j1;
+      bad |= !(l < kInf) ? 1u : 0u;
+      if (l > -kInf) {
+        const double w = exp(static_cast<double>(l) - static_cast<double>(off));
+        s0 += w;
+        t1 += w * static_cast<double>(l);
+        if (own && w > 0.0) {
+          ws += w;
+          if (lmax > -kInf) wu += w * ((static_cast<double>(u) - static_cast<double>(lmax)) * static_cast<double>(c));
+        }
+      }
+      if (own && lmax > -kInf) zl += ex2((u - lmax) * c);
+    }
+    mine.ml = lmax;
+    mine.zl = warp_sum(zl);
+    mine.w = warp_sum(ws);
+    mine.wu = warp_sum(wu);
+    s0 = warp_sum(s0);
+    t1 = warp_sum(t1);
+    mine.bad = __reduce_or_sync(0xffffffffu, bad);
+    if (lane == 0) {
+      sh.s0 = s0;
+      sh.t1 = t1;
+      sh.tnorm = tail ? 0.0 : static_cast<double>(off) + log(s0);
+      sh.at = tail ? fmax(0.0, 1.0 - s0) : 0.0;
+    }
+  } else {
+    // the slice: each thread's maximum, then its sum below that
+    float m = -kInf;
+    for (int g = tid - 32; g < groups; g += kSSlice) {
+      Eight<Raw> v;
+      v.load(buf + g * 8);
+      m = max_nan(m, max8(v));
+    }
+    float z = 0.f;
+    if (m > -kInf && m < kInf) {
+      const f32x2 c2 = pack2(c, c), m2 = pack2(-m, -m);
+      f32x2 z2 = pack2(0.f, 0.f);
+      for (int g = tid - 32; g < groups; g += kSSlice) {
+        Eight<Raw> v;
+        v.load(buf + g * 8);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          float a, b;
+          unpack2(mul2(add2(pair_of(v, i), m2), c2), a, b);
+          z2 = add2(z2, pack2(ex2(a), ex2(b)));
+        }
+      }
+      float a, b;
+      unpack2(z2, a, b);
+      z = a + b;
+    }
+    const float wm = warp_max_nan(m);  // a NaN or +inf marks the part
+    z = warp_sum(z != 0.f ? z * ex2((m - wm) * c) : 0.f);
+    if (lane == 0) sh.red[tid >> 5] = make_float2(wm, z);
+  }
+  cta_sync();
+  asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
+  if (tid < 32) {
+    float2 r = lane > 0 && lane < kSWarps ? sh.red[lane] : make_float2(-kInf, 0.f);
+    mine.mr = warp_max_nan(r.x);
+    mine.zr = warp_sum(r.y != 0.f ? r.y * ex2((r.x - mine.mr) * c) : 0.f);
+    mine.bad |= sh.bad | (mine.mr < kInf ? 0u : 1u);
+    if (lane < (GRAD ? C : 1)) push_part(peer_addr(&sh.parts[rank], lane), peer_addr(&sh.xbar, lane), mine);
+  }
+  if (!GRAD && rank != 0) return;  // nothing is pushed here
+
+  // the row's sums, by the first warp: lane r takes CTA r's part, a fixed tree
+  if (tid < 32) {
+    const bool got = mbar_wait(&sh.xbar, 0);
+    __syncwarp();
+    const DistillPart p = lane < C && got ? sh.parts[lane] : DistillPart{-kInf, 0.f, -kInf, 0.f, 0.0, 0.0, 0u, {0u, 0u, 0u}};
+    const float a = warp_max_nan(fmaxf(p.mr, -kInf)), b = warp_max_nan(fmaxf(p.mr, p.ml));
+    // sums below the references (a: outside the list, b: the row)
+    const float za = warp_sum(p.zr != 0.f ? p.zr * ex2((p.mr - a) * c) : 0.f);
+    const float zb = warp_sum((p.zr != 0.f ? p.zr * ex2((p.mr - b) * c) : 0.f) +
+                              (p.zl != 0.f ? p.zl * ex2((p.ml - b) * c) : 0.f));
+    // sum of the teacher's weight times (l - b) c
+    const double su = warp_sum(p.w > 0.0 ? p.wu + p.w * ((static_cast<double>(p.ml) - static_cast<double>(b)) * static_cast<double>(c)) : 0.0);
+    uint32_t bad = __reduce_or_sync(0xffffffffu, p.bad) | (got ? 0u : 2u);
+    if (!(zb > 0.f)) bad |= 1u;  // every logit masked, or NaN
+    const bool empty = sh.any == 0u || (!tail && !(sh.s0 > 0.0));
+    const bool live = fine && !bad && !empty;
+    const bool outside = tail && za > 0.f;
+    if (lane == 0) {
+      DistillCtx k{};
+      k.c = c;
+      k.inv_t = 1.f / t;
+      k.rall = b;
+      k.lall = log2f(zb);
+      k.ref = outside ? a : b;
+      k.lz = outside ? log2f(za) : k.lall;
+      k.coef = tail ? (outside ? static_cast<float>(static_cast<double>(exp2f((a - b) * c) * za / zb) - sh.at) : 0.f) : 1.f;
+      k.tnorm = static_cast<float>(sh.tnorm);
+      k.zero = live ? 0u : 1u;
+      k.dup = sh.dup;
+      sh.k = k;
+    }
+    __syncwarp();
+    if (GRAD) asm volatile("bar.arrive 1, %0;" ::"n"(kSThreads) : "memory");  // the other warps go on with the gradient
+    if (rank == 0 && lane == 0) {
+      constexpr double kLn2d = 0.69314718055994530942;
+      const double norm = tail ? 1.0 : 1.0 / sh.s0;  // a = w * norm
+      const double lz = log2(static_cast<double>(zb));
+      double loss = (sh.t1 - sh.s0 * sh.tnorm + kLn2d * (lz * sh.s0 - su)) * norm;
+      if (tail && sh.at > 0.0 && za > 0.f) {
+        const double lq = (static_cast<double>(a) - static_cast<double>(b)) * c + log2(static_cast<double>(za)) - lz;
+        loss += sh.at * (log(sh.at) - kLn2d * lq);
+      }
+      if (P.loss) P.loss[row] = (!fine || bad) ? __int_as_float(0x7FC00000) : (empty ? 0.f : static_cast<float>(loss));
+      if (P.valid) P.valid[row] = live ? 1 : 0;
+      if (P.status)
+        P.status[row] = sh.status | (sh.dup ? VS_ROW_DUP_SUPPORT_ID : 0u) | (bad & 2u ? VS_ROW_DEVICE_TIMEOUT : 0u) |
+                        (!fine ? VS_ROW_BAD_PARAM : bad ? VS_ROW_NONFINITE_INPUT : empty ? VS_ROW_EMPTY_SUPPORT : 0u);
+      if (P.ctx) static_cast<DistillCtx*>(P.ctx)[row] = sh.k;
+    }
+    __syncwarp();
+  } else if (GRAD) {
+    asm volatile("bar.sync 1, %0;" ::"n"(kSThreads) : "memory");
+  }
+  if constexpr (GRAD) {
+    const DistillCtx k = sh.k;
+    G* out = static_cast<G*>(P.dlogits) + static_cast<int64_t>(row) * P.grad_ld;
+    const float scale = k.zero ? 0.f : (P.g_loss ? P.g_loss[row] : 1.f) * k.inv_t;
+    const float dense = scale * k.coef;
+    const f32x2 c2 = pack2(k.c, k.c), r2 = pack2(-k.ref, -k.ref), l2 = pack2(-k.lz, -k.lz), d2 = pack2(dense, dense);
+    for (int g = tid; g < groups; g += kSThreads) {
+      Eight<Raw> v;
+      v.load(buf + g * 8);
+      float d[8];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        float a, b;
+        unpack2(fma2(add2(pair_of(v, i), r2), c2, l2), a, b);
+        unpack2(mul2(pack2(ex2(a), ex2(b)), d2), d[2 * i], d[2 * i + 1]);
+      }
+      if (k.zero) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) d[i] = 0.f;
+      }
+      const int j = j0 + g * 8;
+      if (j + 8 <= j1) {
+        Eight<G> o;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) o.e[i] = to_grad<G>(d[i]);
+        o.store(out + j);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (j + i < j1) out[j + i] = to_grad<G>(d[i]);
+      }
+    }
+    cta_sync();
+    if (!k.zero)
+      for (int s = tid; s < W; s += kSThreads) {
+        const int id = ids[s];
+        if (id >= j0 && id < j1)
+          out[id] = to_grad<G>(scale * (ex2(fmaf(us[s] - k.rall, k.c, -k.lall)) - expf(lps[s] - k.tnorm)));
+      }
+  }
+}
+
 template <typename Raw, typename G, bool ACC>
 __global__ void __launch_bounds__(kBThreads) distill_bwd_kernel(DistillParams P, int nchunks) {
   const int row = static_cast<int>(blockIdx.x / nchunks), part = static_cast<int>(blockIdx.x % nchunks);
@@ -397,15 +784,13 @@ __global__ void __launch_bounds__(kBThreads) distill_bwd_kernel(DistillParams P,
   grad_pass<Raw, G, ACC, kBThreads>(x, out, j0, j1, k, g, P.ids + at, P.lp + at, P.width);
 }
 
-template <typename Raw, typename G, bool GRAD>
-cudaError_t launch_fwd(const DistillParams& P, int c, cudaStream_t s) {
-  const size_t smem = sizeof(DistillShared) + (static_cast<size_t>(P.vocab) + 127) / 128 * 16;
-  cudaError_t e = cudaFuncSetAttribute(distill_fwd_kernel<Raw, G, GRAD>,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+template <typename K>
+cudaError_t launch_cluster(K kernel, const DistillParams& P, int c, int threads, size_t smem, cudaStream_t s) {
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(static_cast<unsigned>(P.rows) * c);
-  cfg.blockDim = dim3(kDThreads);
+  cfg.blockDim = dim3(threads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
@@ -415,21 +800,44 @@ cudaError_t launch_fwd(const DistillParams& P, int c, cudaStream_t s) {
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, distill_fwd_kernel<Raw, G, GRAD>, P);
+  return cudaLaunchKernelEx(&cfg, kernel, P);
 }
 
 }  // namespace
 
-cudaError_t launch_distill_fwd(DistillParams P, vs_dtype dtype, vs_dtype dl_dtype, cudaStream_t s) {
-  const int c = row_cluster_size(P.rows, P.vocab);
+// The staged kernel's cluster: slices of at most 40 KB, so that five CTAs share
+// an SM and their phases overlap; smaller ones while the GPU has SMs to spare;
+// 0 when eight slices do not fit shared memory.
+static int stage_cluster_size(int rows, int vocab, int esize) {
+  const int64_t bytes = static_cast<int64_t>(vocab) * esize;
+  int c = 1;
+  while (c < kSMaxCluster && bytes > c * (40 << 10)) c *= 2;
+  while (c < kSMaxCluster && 2ll * c * rows <= 148 && bytes > c * (8 << 10)) c *= 2;
+  return (bytes + c - 1) / c <= (200 << 10) ? c : 0;
+}
+
+template <typename Raw, typename G, bool GRAD>
+static cudaError_t launch_any(DistillParams P, cudaStream_t s) {
+  const int c = stage_cluster_size(P.rows, P.vocab, sizeof(Raw));
+  if (c == 0) {
+    const int f = row_cluster_size(P.rows, P.vocab);
+    P.chunk = ((P.vocab + f - 1) / f + 31) / 32 * 32;
+    const size_t smem = sizeof(DistillShared) + (static_cast<size_t>(P.vocab) + 127) / 128 * 16;
+    return launch_cluster(distill_fwd_kernel<Raw, G, GRAD>, P, f, kDThreads, smem, s);
+  }
   P.chunk = ((P.vocab + c - 1) / c + 31) / 32 * 32;
+  const size_t smem = stage_fixed(P.width) + static_cast<size_t>(P.chunk) * sizeof(Raw);
+  return launch_cluster(distill_stage_kernel<Raw, G, GRAD>, P, c, kSThreads, smem, s);
+}
+
+cudaError_t launch_distill_fwd(DistillParams P, vs_dtype dtype, vs_dtype dl_dtype, cudaStream_t s) {
   const bool grad = P.dlogits != nullptr, half = dl_dtype == VS_BF16;
   if (dtype == VS_BF16) {
-    if (!grad) return launch_fwd<uint16_t, float, false>(P, c, s);
-    return half ? launch_fwd<uint16_t, uint16_t, true>(P, c, s) : launch_fwd<uint16_t, float, true>(P, c, s);
+    if (!grad) return launch_any<uint16_t, float, false>(P, s);
+    return half ? launch_any<uint16_t, uint16_t, true>(P, s) : launch_any<uint16_t, float, true>(P, s);
   }
-  if (!grad) return launch_fwd<uint32_t, float, false>(P, c, s);
-  return half ? launch_fwd<uint32_t, uint16_t, true>(P, c, s) : launch_fwd<uint32_t, float, true>(P, c, s);
+  if (!grad) return launch_any<uint32_t, float, false>(P, s);
+  return half ? launch_any<uint32_t, uint16_t, true>(P, s) : launch_any<uint32_t, float, true>(P, s);
 }
 
 cudaError_t launch_distill_bwd(DistillParams P, vs_dtype dtype, vs_dtype dl_dtype, bool acc, cudaStream_t s) {

@@ -110,6 +110,16 @@ def test_benchmark_vocabulary(dtype, rows):
     check(x, ids, lp, 1.0, True)
 
 
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_vocabularies_beyond_shared_memory(dtype):
+    """The largest vocabulary, whose row no cluster's shared memory holds, and
+    one in between with an odd end."""
+    for vocab in (1 << 20, 640_003):
+        x = logits_on("cuda", 3, vocab, dtype, seed=5)
+        ids, lp = lists(3, vocab, 300, seed=6, x=x[:, :vocab])
+        check(x, ids, lp, 0.9, True, None, vocab)
+
+
 @pytest.mark.parametrize("tail", [False, True])
 @pytest.mark.parametrize("grad_dtype", [BF, F32])
 def test_accumulates(tail, grad_dtype):
@@ -164,6 +174,24 @@ def test_small_shares_outside_the_list(dtype):
     lp = torch.log(torch.tensor([[.7, .1, .05], [.999, 1e-4, 1e-4], [.5, .4, .1]])).cuda()
     check(x, ids, lp, 1.0, True)
     check(x, ids, lp, 1.0, False)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("tail", [False, True])
+def test_values_at_the_ends_of_the_type(dtype, tail):
+    """Rows whose logits times log2(e) / T overflow fp32: all at the lowest
+    value (uniform), tokens masked by it, and both ends in one row."""
+    vocab, low = 1003, -torch.finfo(dtype).max
+    x = logits_on("cuda", 4, vocab, dtype, seed=23, spikes=0)
+    x[0, :vocab] = low
+    x[1, 20:vocab] = low
+    x[2, :vocab] = -low
+    x[3, 7:vocab:3] = low
+    x[3, 0:vocab:2] = -low
+    ids = torch.tensor([[0, 5, 900], [3, 19, 18], [1, 2, 1002], [0, 2, 4]], dtype=torch.int32).cuda()
+    lp = torch.log(torch.tensor([[.5, .2, .1]] * 4)).cuda()
+    for t in (0.5, 1.0):
+        check(x, ids, lp, t, tail, None, vocab)
 
 
 def test_identical_teacher_and_student():
