@@ -23,6 +23,7 @@
 
 #include "common.cuh"
 #include "internal.h"
+#include "row_stage.cuh"
 
 namespace vs {
 
@@ -57,21 +58,6 @@ __device__ __forceinline__ G to_grad(float v) {
   else
     return v;
 }
-
-// Eight elements of a row from j (a multiple of 8; j + 8 <= the row's end).
-template <typename T>
-union Eight {
-  uint4 q[sizeof(T) / 2];
-  T e[8];
-  __device__ __forceinline__ void load(const T* p) {
-#pragma unroll
-    for (int i = 0; i < static_cast<int>(sizeof(T)) / 2; ++i) q[i] = reinterpret_cast<const uint4*>(p)[i];
-  }
-  __device__ __forceinline__ void store(T* p) const {
-#pragma unroll
-    for (int i = 0; i < static_cast<int>(sizeof(T)) / 2; ++i) reinterpret_cast<uint4*>(p)[i] = q[i];
-  }
-};
 
 // Slot s of a list is its id's first occurrence.
 __device__ __forceinline__ bool first_of(const int32_t* ids, int s) {
@@ -432,66 +418,6 @@ __host__ __device__ inline size_t stage_fixed(int width) {
   return sizeof(DistillStage) + 12 * static_cast<size_t>(stage_width(width)) + 4 * static_cast<size_t>(stage_hash(width));
 }
 
-__device__ __forceinline__ float max_nan(float a, float b) {
-  float r;
-  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
-  return r;
-}
-
-// Largest of eight elements (NaN if there is one).
-__device__ __forceinline__ float max8(const Eight<uint16_t>& v) {
-  uint32_t m = 0xFF80FF80u;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const uint32_t w = reinterpret_cast<const uint32_t*>(v.q)[i];
-    const __nv_bfloat162 r = __hmax2_nan(*reinterpret_cast<const __nv_bfloat162*>(&m),
-                                         *reinterpret_cast<const __nv_bfloat162*>(&w));
-    m = *reinterpret_cast<const uint32_t*>(&r);
-  }
-  return max_nan(__uint_as_float(m << 16), __uint_as_float(m & 0xFFFF0000u));
-}
-__device__ __forceinline__ float max8(const Eight<uint32_t>& v) {
-  float m = __uint_as_float(v.e[0]);
-#pragma unroll
-  for (int i = 1; i < 8; ++i) m = max_nan(m, __uint_as_float(v.e[i]));
-  return m;
-}
-__device__ __forceinline__ f32x2 pair_of(const Eight<uint16_t>& v, int i) {
-  const uint32_t w = reinterpret_cast<const uint32_t*>(v.q)[i];
-  return pack2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
-}
-__device__ __forceinline__ f32x2 pair_of(const Eight<uint32_t>& v, int i) {
-  return pack2(__uint_as_float(v.e[2 * i]), __uint_as_float(v.e[2 * i + 1]));
-}
-
-template <typename T>
-__device__ __forceinline__ T warp_sum(T x) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-  return x;
-}
-__device__ __forceinline__ float warp_max_nan(float x) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) x = max_nan(x, __shfl_xor_sync(0xffffffffu, x, o));
-  return x;
-}
-
-// A part into a peer's shared memory, counted on its barrier.
-__device__ __forceinline__ uint32_t peer_addr(const void* p, uint32_t rank) {
-  uint32_t r;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(smem_addr(p)), "r"(rank));
-  return r;
-}
-__device__ __forceinline__ void push_part(uint32_t dst, uint32_t bar, const DistillPart& p) {
-  const uint32_t* w = reinterpret_cast<const uint32_t*>(&p);
-#pragma unroll
-  for (int i = 0; i < 3; ++i)
-    asm volatile(
-        "st.async.shared::cluster.mbarrier::complete_tx::bytes.v4.b32 [%0], {%2, %3, %4, %5}, [%1];" ::"r"(dst + 16u * i),
-        "r"(bar), "r"(w[4 * i]), "r"(w[4 * i + 1]), "r"(w[4 * i + 2]), "r"(w[4 * i + 3])
-        : "memory");
-}
-
 template <typename Raw, typename G, bool GRAD>
 __global__ void __launch_bounds__(kSThreads, 5) distill_stage_kernel(DistillParams P) {
   extern __shared__ __align__(16) unsigned char d_smem[];
@@ -525,9 +451,13 @@ __global__ void __launch_bounds__(kSThreads, 5) distill_stage_kernel(DistillPara
     }
     sh.status = sh.dup = sh.any = sh.bad = 0u;
   }
+  // this thread's first slot of the list, on its way during the set-up
+  const int64_t list_at = static_cast<int64_t>(row) * P.teacher_ld;
+  const int32_t id0 = tid < W ? P.ids[list_at + tid] : -1;
+  const float lp0 = tid < W ? P.lp[list_at + tid] : 0.f;
   // the parts' barriers are ready everywhere once every CTA has arrived here
   __syncwarp();
-  asm volatile("barrier.cluster.arrive.aligned;" ::: "memory");
+  asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");  // ordered by the fence above
   const float t = P.temperature ? P.temperature[row] : P.temperature_scalar;
   const bool fine = t > 0.f && t < kInf;
   const float c = fminf(kLog2e / t, 3e38f);
@@ -538,9 +468,8 @@ __global__ void __launch_bounds__(kSThreads, 5) distill_stage_kernel(DistillPara
   for (int i = tid; i < hsize / 4; i += kSThreads) reinterpret_cast<int4*>(hash)[i] = make_int4(-1, -1, -1, -1);
   cta_sync();
   for (int s = tid; s < W; s += kSThreads) {
-    const int64_t at = static_cast<int64_t>(row) * P.teacher_ld + s;
-    int32_t id = P.ids[at];
-    lps[s] = P.lp[at];
+    int32_t id = s == tid ? id0 : P.ids[list_at + s];
+    lps[s] = s == tid ? lp0 : P.lp[list_at + s];
     if (id < -1 || id >= V) {
       atomicOr(&sh.status, VS_ROW_BAD_SUPPORT_ID);
       id = -1;
@@ -577,15 +506,14 @@ __global__ void __launch_bounds__(kSThreads, 5) distill_stage_kernel(DistillPara
   // take this slice's listed elements out of the copy
   if (bytes && !mbar_wait(&sh.bar, 0)) atomicOr(&sh.bad, 2u);
   __syncwarp();
-  for (int s = tid; s < W; s += kSThreads) {
+  for (int s = tid; s < W; s += kSThreads) {  // repeats are off the list: no two slots name one element
     const int id = ids[s];
-    const bool own = id >= j0 && id < j1;
-    us[s] = own ? value_of(buf[id - j0]) : -kInf;
-  }
-  cta_sync();  // a repeated id's slots are gone, so no two slots name one element
-  for (int s = tid; s < W; s += kSThreads) {
-    const int id = ids[s];
-    if (id >= j0 && id < j1) buf[id - j0] = kMasked;
+    float u = -kInf;
+    if (id >= j0 && id < j1) {
+      u = value_of(buf[id - j0]);
+      buf[id - j0] = kMasked;
+    }
+    us[s] = u;
   }
   cta_sync();
 
@@ -637,31 +565,8 @@ __global__ void __launch_bounds__(kSThreads, 5) distill_stage_kernel(DistillPara
       sh.at = tail ? fmax(0.0, 1.0 - s0) : 0.0;
     }
   } else {
-    // the slice: each thread's maximum, then its sum below that
-    float m = -kInf;
-    for (int g = tid - 32; g < groups; g += kSSlice) {
-      Eight<Raw> v;
-      v.load(buf + g * 8);
-      m = max_nan(m, max8(v));
-    }
-    float z = 0.f;
-    if (m > -kInf && m < kInf) {
-      const f32x2 c2 = pack2(c, c), m2 = pack2(-m, -m);
-      f32x2 z2 = pack2(0.f, 0.f);
-      for (int g = tid - 32; g < groups; g += kSSlice) {
-        Eight<Raw> v;
-        v.load(buf + g * 8);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          float a, b;
-          unpack2(mul2(add2(pair_of(v, i), m2), c2), a, b);
-          z2 = add2(z2, pack2(ex2(a), ex2(b)));
-        }
-      }
-      float a, b;
-      unpack2(z2, a, b);
-      z = a + b;
-    }
+    float m, z;
+    slice_sum(buf, tid - 32, groups, kSSlice, c, m, z);
     const float wm = warp_max_nan(m);  // a NaN or +inf marks the part
     z = warp_sum(z != 0.f ? z * ex2((m - wm) * c) : 0.f);
     if (lane == 0) sh.red[tid >> 5] = make_float2(wm, z);
@@ -673,7 +578,7 @@ __global__ void __launch_bounds__(kSThreads, 5) distill_stage_kernel(DistillPara
     mine.mr = warp_max_nan(r.x);
     mine.zr = warp_sum(r.y != 0.f ? r.y * ex2((r.x - mine.mr) * c) : 0.f);
     mine.bad |= sh.bad | (mine.mr < kInf ? 0u : 1u);
-    if (lane < (GRAD ? C : 1)) push_part(peer_addr(&sh.parts[rank], lane), peer_addr(&sh.xbar, lane), mine);
+    if (lane < (GRAD ? C : 1)) push_words<sizeof(DistillPart) / 16>(peer_addr(&sh.parts[rank], lane), peer_addr(&sh.xbar, lane), &mine);
   }
   if (!GRAD && rank != 0) return;  // nothing is pushed here
 
@@ -735,7 +640,12 @@ __global__ void __launch_bounds__(kSThreads, 5) distill_stage_kernel(DistillPara
     G* out = static_cast<G*>(P.dlogits) + static_cast<int64_t>(row) * P.grad_ld;
     const float scale = k.zero ? 0.f : (P.g_loss ? P.g_loss[row] : 1.f) * k.inv_t;
     const float dense = scale * k.coef;
-    const f32x2 c2 = pack2(k.c, k.c), r2 = pack2(-k.ref, -k.ref), l2 = pack2(-k.lz, -k.lz), d2 = pack2(dense, dense);
+    // one fused multiply-add per exponent: l c - (ref c + lz), the constant's rounding in the factor
+    const double shift = static_cast<double>(k.ref) * k.c + static_cast<double>(k.lz);
+    const float sf = static_cast<float>(shift);
+    const bool wide = !(fabsf(sf) < 1e37f);  // l c may overflow: the differences first
+    const float lead = wide ? dense : dense * exp2f(static_cast<float>(static_cast<double>(sf) - shift));
+    const f32x2 c2 = pack2(k.c, k.c), s2 = pack2(-sf, -sf), d2 = pack2(lead, lead);
     for (int g = tid; g < groups; g += kSThreads) {
       Eight<Raw> v;
       v.load(buf + g * 8);
@@ -743,12 +653,13 @@ __global__ void __launch_bounds__(kSThreads, 5) distill_stage_kernel(DistillPara
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         float a, b;
-        unpack2(fma2(add2(pair_of(v, i), r2), c2, l2), a, b);
+        unpack2(fma2(pair_of(v, i), c2, s2), a, b);
         unpack2(mul2(pack2(ex2(a), ex2(b)), d2), d[2 * i], d[2 * i + 1]);
       }
-      if (k.zero) {
+      if (k.zero || wide) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) d[i] = 0.f;
+        for (int i = 0; i < 8; ++i)
+          d[i] = k.zero ? 0.f : dense * ex2(fmaf(value_of(v.e[i]) - k.ref, k.c, -k.lz));
       }
       const int j = j0 + g * 8;
       if (j + 8 <= j1) {
@@ -784,37 +695,7 @@ __global__ void __launch_bounds__(kBThreads) distill_bwd_kernel(DistillParams P,
   grad_pass<Raw, G, ACC, kBThreads>(x, out, j0, j1, k, g, P.ids + at, P.lp + at, P.width);
 }
 
-template <typename K>
-cudaError_t launch_cluster(K kernel, const DistillParams& P, int c, int threads, size_t smem, cudaStream_t s) {
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
-  if (e != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(static_cast<unsigned>(P.rows) * c);
-  cfg.blockDim = dim3(threads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = s;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = c;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, P);
-}
-
 }  // namespace
-
-// The staged kernel's cluster: slices of at most 40 KB, so that five CTAs share
-// an SM and their phases overlap; smaller ones while the GPU has SMs to spare;
-// 0 when eight slices do not fit shared memory.
-static int stage_cluster_size(int rows, int vocab, int esize) {
-  const int64_t bytes = static_cast<int64_t>(vocab) * esize;
-  int c = 1;
-  while (c < kSMaxCluster && bytes > c * (40 << 10)) c *= 2;
-  while (c < kSMaxCluster && 2ll * c * rows <= 148 && bytes > c * (8 << 10)) c *= 2;
-  return (bytes + c - 1) / c <= (200 << 10) ? c : 0;
-}
 
 template <typename Raw, typename G, bool GRAD>
 static cudaError_t launch_any(DistillParams P, cudaStream_t s) {
@@ -823,11 +704,11 @@ static cudaError_t launch_any(DistillParams P, cudaStream_t s) {
     const int f = row_cluster_size(P.rows, P.vocab);
     P.chunk = ((P.vocab + f - 1) / f + 31) / 32 * 32;
     const size_t smem = sizeof(DistillShared) + (static_cast<size_t>(P.vocab) + 127) / 128 * 16;
-    return launch_cluster(distill_fwd_kernel<Raw, G, GRAD>, P, f, kDThreads, smem, s);
+    return launch_cluster(distill_fwd_kernel<Raw, G, GRAD>, P, static_cast<unsigned>(P.rows) * f, f, kDThreads, smem, s);
   }
   P.chunk = ((P.vocab + c - 1) / c + 31) / 32 * 32;
   const size_t smem = stage_fixed(P.width) + static_cast<size_t>(P.chunk) * sizeof(Raw);
-  return launch_cluster(distill_stage_kernel<Raw, G, GRAD>, P, c, kSThreads, smem, s);
+  return launch_cluster(distill_stage_kernel<Raw, G, GRAD>, P, static_cast<unsigned>(P.rows) * c, c, kSThreads, smem, s);
 }
 
 cudaError_t launch_distill_fwd(DistillParams P, vs_dtype dtype, vs_dtype dl_dtype, cudaStream_t s) {

@@ -1,0 +1,175 @@
+// Rows staged in shared memory: helpers of the kernels whose cluster copies a
+// row's slices into its CTAs' shared memory once and passes over that copy.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <stdint.h>
+
+#include "common.cuh"
+
+namespace vs {
+
+// Eight elements of a row from j (a multiple of 8; j + 8 <= the row's end).
+template <typename T>
+union Eight {
+  uint4 q[sizeof(T) / 2];
+  T e[8];
+  __device__ __forceinline__ void load(const T* p) {
+#pragma unroll
+    for (int i = 0; i < static_cast<int>(sizeof(T)) / 2; ++i) q[i] = reinterpret_cast<const uint4*>(p)[i];
+  }
+  __device__ __forceinline__ void store(T* p) const {
+#pragma unroll
+    for (int i = 0; i < static_cast<int>(sizeof(T)) / 2; ++i) reinterpret_cast<uint4*>(p)[i] = q[i];
+  }
+};
+
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
+// Largest of eight elements (NaN if there is one).
+__device__ __forceinline__ float max8(const Eight<uint16_t>& v) {
+  uint32_t m = 0xFF80FF80u;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t w = reinterpret_cast<const uint32_t*>(v.q)[i];
+    const __nv_bfloat162 r = __hmax2_nan(*reinterpret_cast<const __nv_bfloat162*>(&m),
+                                         *reinterpret_cast<const __nv_bfloat162*>(&w));
+    m = *reinterpret_cast<const uint32_t*>(&r);
+  }
+  return max_nan(__uint_as_float(m << 16), __uint_as_float(m & 0xFFFF0000u));
+}
+__device__ __forceinline__ float max8(const Eight<uint32_t>& v) {
+  float m = __uint_as_float(v.e[0]);
+#pragma unroll
+  for (int i = 1; i < 8; ++i) m = max_nan(m, __uint_as_float(v.e[i]));
+  return m;
+}
+__device__ __forceinline__ f32x2 pair_of(const Eight<uint16_t>& v, int i) {
+  const uint32_t w = reinterpret_cast<const uint32_t*>(v.q)[i];
+  return pack2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+}
+__device__ __forceinline__ f32x2 pair_of(const Eight<uint32_t>& v, int i) {
+  return pack2(__uint_as_float(v.e[2 * i]), __uint_as_float(v.e[2 * i + 1]));
+}
+
+template <typename T>
+__device__ __forceinline__ T warp_sum(T x) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+  return x;
+}
+__device__ __forceinline__ float warp_max_nan(float x) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) x = max_nan(x, __shfl_xor_sync(0xffffffffu, x, o));
+  return x;
+}
+
+__device__ __forceinline__ uint32_t peer_addr(const void* p, uint32_t rank) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(smem_addr(p)), "r"(rank));
+  return r;
+}
+// N 16-byte words into a peer's shared memory, counted on its barrier there.
+template <int N>
+__device__ __forceinline__ void push_words(uint32_t dst, uint32_t bar, const void* src) {
+  const uint32_t* w = static_cast<const uint32_t*>(src);
+#pragma unroll
+  for (int i = 0; i < N; ++i)
+    asm volatile(
+        "st.async.shared::cluster.mbarrier::complete_tx::bytes.v4.b32 [%0], {%2, %3, %4, %5}, [%1];" ::"r"(dst + 16u * i),
+        "r"(bar), "r"(w[4 * i]), "r"(w[4 * i + 1]), "r"(w[4 * i + 2]), "r"(w[4 * i + 3])
+        : "memory");
+}
+
+// A thread's share of a staged slice, the groups of eight g0, g0 + step, ..:
+// z = sum of 2^((l - m) c) below a reference m.  The first group's maximum
+// serves as long as the sum stays moderate (a sum of powers of two keeps its
+// relative precision whatever the reference), which saves a pass; one fused
+// multiply-add per exponent, the rounding of m c put back after.  Masked
+// first groups, far larger values later, and l c that overflows take the
+// thread's maximum and the differences first.  A NaN or +inf comes out as m.
+template <typename Raw>
+__device__ __forceinline__ void slice_sum(const Raw* buf, int g0, int groups, int step, float c, float& m, float& z) {
+  m = -kInf;
+  z = 0.f;
+  if (g0 >= groups) return;
+  {
+    Eight<Raw> v;
+    v.load(buf + g0 * 8);
+    m = max8(v);
+  }
+  const float mc = __fmul_rn(m, c);
+  if (fabsf(mc) < 1e37f) {
+    const f32x2 c2 = pack2(c, c), m2 = pack2(-mc, -mc);
+    f32x2 z2 = pack2(0.f, 0.f), y2 = pack2(0.f, 0.f);
+    for (int g = g0; g < groups; g += step) {
+      Eight<Raw> v;
+      v.load(buf + g * 8);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        float a, b;
+        unpack2(fma2(pair_of(v, i), c2, m2), a, b);
+        if (i & 1)
+          y2 = add2(y2, pack2(ex2(a), ex2(b)));
+        else
+          z2 = add2(z2, pack2(ex2(a), ex2(b)));
+      }
+    }
+    float a, b;
+    unpack2(add2(z2, y2), a, b);
+    z = (a + b) * ex2(-fmaf(m, c, -mc));
+  }
+  if (z > 0.f && z < 1e30f) return;
+  z = 0.f;
+  m = -kInf;
+  for (int g = g0; g < groups; g += step) {
+    Eight<Raw> v;
+    v.load(buf + g * 8);
+    m = max_nan(m, max8(v));
+  }
+  if (m > -kInf && m < kInf)
+    for (int g = g0; g < groups; g += step) {
+      Eight<Raw> v;
+      v.load(buf + g * 8);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) z += ex2((value_of(v.e[i]) - m) * c);
+    }
+}
+
+// Cluster size of a staged kernel: slices of at most 40 KB, so that several
+// CTAs share an SM and their phases overlap; smaller ones while the GPU has SMs
+// to spare; 0 when eight slices do not fit shared memory.
+inline int stage_cluster_size(int rows, int vocab, int esize) {
+  constexpr int kMost = 8;
+  const int64_t bytes = static_cast<int64_t>(vocab) * esize;
+  int c = 1;
+  while (c < kMost && bytes > c * (40 << 10)) c *= 2;
+  while (c < kMost && 2ll * c * rows <= 148 && bytes > c * (8 << 10)) c *= 2;
+  return (bytes + c - 1) / c <= (200 << 10) ? c : 0;
+}
+
+// Launch `kernel` with clusters of c CTAs.
+template <typename K, typename P>
+cudaError_t launch_cluster(K kernel, const P& params, unsigned grid, int c, int threads, size_t smem, cudaStream_t s) {
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = c;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, params);
+}
+
+}  // namespace vs
