@@ -14,7 +14,7 @@ INCLUDE = PKG.parent / "include"
 LIB = PKG / "libvs.so"
 
 SOURCES = ["api.cu", "score_fwd.cu", "score_row.cu", "score_bwd.cu", "l1_distance.cu", "fused_lmhead.cu", "support_head.cu",
-           "sample.cu", "distill.cu"]
+           "sample.cu", "row_list.cu", "distill.cu"]
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 
 

@@ -110,8 +110,28 @@ struct SampleParams {
   float* logprob;
   int32_t* support_size;
   uint32_t* status;
-  int32_t fx_shift;  // fixed-point scale of the masses: vocab * 2^fx_shift <= 2^63
+  int32_t fx_shift;  // fixed-point scale of the masses: vocab * 2^fx_shift <= 2^62
+  int32_t lists;     // the list kernel has gone through the rows with a small top-k
 };
+
+// A list row that the list kernel leaves to the general one (in token[row], ids[row, 0]).
+constexpr int32_t kListLeft = -2;
+// Largest top-k of vs_sample that is taken from a list of the row's largest
+// elements.  A greedy row is one of them.
+constexpr int kListTopK = 512;
+__host__ __device__ inline int sample_list_k(int vocab, float t, int top_k) {
+  if (t == 0.f) return 1;
+  return top_k > 0 && top_k < vocab && top_k <= kListTopK ? top_k : 0;
+}
+#ifdef __CUDACC__
+// The running mass that a row's number asks for: the first integer above
+// u * mass, at most the mass itself (u = 1 takes the last token).
+__device__ __forceinline__ unsigned long long draw_target(float u, unsigned long long mass) {
+  const double x = floor(static_cast<double>(u) * static_cast<double>(mass));
+  const unsigned long long t = x >= static_cast<double>(mass) ? mass : static_cast<unsigned long long>(x) + 1ull;
+  return t < mass ? t : mass;
+}
+#endif
 
 struct TopkParams {
   int32_t rows, vocab, k;
@@ -123,6 +143,7 @@ struct TopkParams {
   float* logprob;
   uint32_t* status;
   int32_t fx_shift;
+  int32_t lists;  // as above
 };
 
 struct DistillParams {
@@ -148,6 +169,9 @@ int row_cluster_size(int rows, int vocab);
 // launchers (return a cudaError_t from the launch)
 cudaError_t launch_sample(const SampleParams& p, vs_dtype dtype, cudaStream_t s);
 cudaError_t launch_topk(const TopkParams& p, vs_dtype dtype, cudaStream_t s);
+// Their list kernels; *done false: the rows do not fit shared memory, nothing was launched.
+cudaError_t launch_sample_list(const SampleParams& p, vs_dtype dtype, cudaStream_t s, bool* done);
+cudaError_t launch_topk_list(const TopkParams& p, vs_dtype dtype, cudaStream_t s, bool* done);
 cudaError_t launch_distill_fwd(DistillParams p, vs_dtype dtype, vs_dtype dl_dtype, cudaStream_t s);
 cudaError_t launch_distill_bwd(DistillParams p, vs_dtype dtype, vs_dtype dl_dtype, bool accumulate,
                                cudaStream_t s);

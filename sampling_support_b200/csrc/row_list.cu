@@ -1,0 +1,541 @@
+// Rows whose answer lies in their first k tokens: the list kernel behind
+// vs_topk_logprob and behind vs_sample's rows with a small top-k.
+//
+// A cluster stages the row in its CTAs' shared memory (one bulk copy per
+// slice, so the row is read from HBM once) and finds a floor that at least k
+// elements reach: every thread's two vector maxima are elements of their own,
+// so a value that k of any CTA's maxima reach is a floor, and so is the smallest
+// over the CTAs of values that ceil(k / C) of theirs reach.  The elements from the floor
+// up (hardly more than k) are listed, gathered by the leader and sorted there.
+// Top-k adds the row's sum of exponentials, taken in the same pass as the
+// maxima; sampling cuts and draws from the sorted masses.
+//
+// Bound: a CTA holds its shared memory for several microseconds of mostly
+// latency (copy, floor, exchange, listing), so with 40 KB slices and five CTAs
+// per SM the rate is that of the slots.  No cluster barrier is waited for: the
+// floors and the first listed elements of every CTA are pushed, and a CTA
+// leaves once they are sent unless it has listed more.  Rows whose list overflows
+// (crowds of equal values) are marked and left to the general kernels.
+#include <algorithm>
+
+#include "internal.h"
+#include "row_stage.cuh"
+#include "select.cuh"
+
+namespace vs {
+
+namespace {
+
+constexpr int kLThreads = 256;
+constexpr int kLWarps = kLThreads / 32;
+constexpr int kLMaxCluster = 8;
+constexpr int kLTotal = 4096;  // listed elements per row, at most
+constexpr int kLBins = 512;    // of the vector maxima, linear in the value below the largest
+// Listed elements per CTA: 256 keep five CTAs on an SM, wide lists take 1,024.
+__host__ __device__ inline int list_local(int k) { return k <= 256 ? 256 : 1024; }
+
+struct alignas(16) ListPart {
+  uint32_t kmax;         // largest key
+  uint32_t kth, share;   // floors that k and ceil(k / C) of the maxima reach
+  float m, z;            // sum of 2^((l - m) c)
+  uint32_t pad[3];
+};
+
+// What a CTA pushes of its list: its length and its first elements, the rest
+// (if any) stays for the leader to fetch.
+constexpr int kLPush = 62;
+struct alignas(16) ListPush {
+  uint32_t n, pad[3];
+  u64 e[kLPush];
+};
+static_assert(sizeof(ListPush) == 32 * 16, "one 16-byte store per lane");
+
+struct alignas(16) ListStage {
+  ListPart parts[kLMaxCluster];
+  union {
+    ListPush pushed[kLMaxCluster];  // leader: from the CTA of each rank
+    struct {                        // before that: no CTA lists before it has this one's part
+      uint32_t bins[kLBins];        // maxima per bin, and the smallest key of each
+      uint32_t least[kLBins];
+    };
+  };
+  ListPush mine;
+  uint64_t bar, xbar, lbar, fbar;  // the slice's copy; the parts; the lists; (listed more) the leader has fetched
+  uint64_t gbar[kLMaxCluster];     // leader: the rest of that CTA's list is written
+  float2 red[kLWarps];
+  uint32_t rmax[kLWarps], rmin[kLWarps];
+  uint32_t bad;
+};
+
+// Shared memory behind it: this CTA's list (key << 32 | ~id) beyond mine.e,
+// then the slice, later the leader's list and its sorted copy.
+__host__ __device__ inline int list_total(int c, int local) { return c * local < kLTotal ? c * local : kLTotal; }
+__host__ __device__ inline size_t list_more(int local) { return static_cast<size_t>(local - kLPush + 1) / 2 * 16; }
+__host__ __device__ inline size_t list_room(int c, int local, size_t slice) {
+  const size_t lists = static_cast<size_t>(list_total(c, local) + kListTopK) * sizeof(u64);
+  return list_more(local) + (slice > lists ? slice : lists);
+}
+
+template <typename Raw>
+struct ListKey {
+  static constexpr uint32_t kMasked = sizeof(Raw) == 2 ? 0x007Fu : 0x007FFFFFu;  // key of -inf
+  __device__ __forceinline__ static uint32_t of(float v) {
+    return sizeof(Raw) == 2 ? key_of(static_cast<uint16_t>(__float_as_uint(v) >> 16)) : key_of(__float_as_uint(v));
+  }
+};
+
+// One warp: the bin in which the running count of the block's maxima reaches k
+// (lane l holds the counts c of kLBins / 32 bins, upto the sum through them);
+// -1 when there are fewer.
+__device__ __forceinline__ int bin_reaching(uint32_t upto, uint32_t mine, const uint32_t (&c)[kLBins / 32], uint32_t k) {
+  const uint32_t hit = __ballot_sync(0xffffffffu, upto >= k);
+  if (!hit) return -1;
+  const int l = __ffs(hit) - 1;
+  uint32_t run = upto - mine;
+  int b = 0;
+#pragma unroll
+  for (int i = 0; i < kLBins / 32; ++i) {
+    run += c[i];
+    if (run < k) b = i + 1;
+  }
+  return __shfl_sync(0xffffffffu, b, l) + l * (kLBins / 32);
+}
+
+// The n listed elements in descending order at `out` (the first `keep`; room
+// for kListTopK) or, for more than a block's worth, sorted in place.  Returns
+// where they are.
+__device__ __forceinline__ u64* list_sort(u64* list, u64* out, uint32_t n, uint32_t keep) {
+  if (n <= kLThreads) {
+    int bits = 3;
+    while ((1u << bits) < n) ++bits;
+    const int g = kLThreads >> bits;  // neighbouring lanes that share an element
+    const uint32_t at = threadIdx.x / g;
+    const u64 e = at < n ? list[at] : 0ull;
+    uint32_t place = 0u;
+    for (uint32_t o = threadIdx.x & (g - 1); o < n; o += g) place += list[o] > e ? 1u : 0u;
+    for (int o = 1; o < g; o <<= 1) place += __shfl_xor_sync(0xffffffffu, place, o);
+    if (at < n && (threadIdx.x & (g - 1)) == 0 && place < keep) out[place] = e;
+    cta_sync();
+    return out;
+  }
+  uint32_t m = 2 * kLThreads;
+  while (m < n) m *= 2;
+  for (uint32_t i = n + threadIdx.x; i < m; i += kLThreads) list[i] = 0ull;
+  for (uint32_t size = 2; size <= m; size <<= 1)
+    for (uint32_t step = size >> 1; step > 0; step >>= 1) {
+      cta_sync();
+      for (uint32_t i = threadIdx.x; i < m / 2; i += kLThreads) {
+        const uint32_t a = 2 * i - (i & (step - 1)), b = a + step;
+        const u64 x = list[a], y = list[b];
+        if (((a & size) == 0u) == (x < y)) {
+          list[a] = y;
+          list[b] = x;
+        }
+      }
+    }
+  cta_sync();
+  return list;
+}
+static_assert(kLThreads <= kListTopK && (kLTotal & (kLTotal - 1)) == 0, "the sorted copy's room, and the padded list's");
+
+// vs_topk_logprob: rows[k] ids and log-probabilities.
+struct TopkOp {
+  using Params = TopkParams;
+  static constexpr bool kSum = true;
+  __device__ __forceinline__ static int k_of(const Params& P, int) { return P.k; }
+  static int most(const Params& P) { return P.k; }
+  __device__ __forceinline__ static float t_of(const Params& P, int row) {
+    return P.temperature ? P.temperature[row] : P.temperature_scalar;
+  }
+  __device__ __forceinline__ static bool fine(const Params& P, int row) {
+    const float t = t_of(P, row);
+    return t > 0.f && t < kInf;
+  }
+  __device__ __forceinline__ static void overflow(const Params& P, int row) {
+    if (threadIdx.x == 0) P.ids[static_cast<int64_t>(row) * P.out_ld] = kListLeft;
+  }
+  // no list: bad input, or every token masked
+  __device__ __forceinline__ static void none(const Params& P, int row, uint32_t status) {
+    int32_t* ids = P.ids + static_cast<int64_t>(row) * P.out_ld;
+    float* lps = P.logprob ? P.logprob + static_cast<int64_t>(row) * P.out_ld : nullptr;
+    const float lp = status == VS_ROW_EMPTY_SUPPORT ? -kInf : __int_as_float(0x7FC00000);
+    for (int i = threadIdx.x; i < P.k; i += kLThreads) {
+      ids[i] = -1;
+      if (lps) lps[i] = lp;
+    }
+    if (threadIdx.x == 0 && P.status) P.status[row] = status;
+  }
+  template <typename Raw>
+  __device__ __forceinline__ static void finish(const Params& P, int row, u64* sorted, u64*, uint32_t nk, float vmax,
+                                                float z) {
+    int32_t* ids = P.ids + static_cast<int64_t>(row) * P.out_ld;
+    float* lps = P.logprob ? P.logprob + static_cast<int64_t>(row) * P.out_ld : nullptr;
+    const float t = t_of(P, row), lz = logf(z);
+    for (int i = threadIdx.x; i < P.k; i += kLThreads) {
+      const bool in = static_cast<uint32_t>(i) < nk;
+      const u64 e = in ? sorted[i] : 0ull;
+      ids[i] = in ? static_cast<int32_t>(~static_cast<uint32_t>(e)) : -1;
+      if (lps) lps[i] = in ? (KeyTraits<Raw>::decode(static_cast<uint32_t>(e >> 32)) - vmax) / t - lz : -kInf;
+    }
+    if (threadIdx.x == 0 && P.status) P.status[row] = 0u;
+  }
+};
+
+// vs_sample's rows with a small top-k (greedy rows among them).
+struct SampleOp {
+  using Params = SampleParams;
+  static constexpr bool kSum = false;
+  static int most(const Params& P) { return P.top_k ? kListTopK : sample_list_k(P.vocab, 1.f, P.top_k_scalar); }
+  __device__ __forceinline__ static float t_of(const Params& P, int row) {
+    return P.temperature ? P.temperature[row] : P.temperature_scalar;
+  }
+  __device__ __forceinline__ static int k_of(const Params& P, int row) {
+    return sample_list_k(P.vocab, t_of(P, row), P.top_k ? P.top_k[row] : P.top_k_scalar);
+  }
+  __device__ __forceinline__ static bool fine(const Params& P, int row) {
+    const float t = t_of(P, row), p = P.top_p ? P.top_p[row] : P.top_p_scalar, m = P.min_p ? P.min_p[row] : P.min_p_scalar;
+    const float u = P.uniform[row];
+    return t >= 0.f && t < kInf && p > 0.f && m <= 1.f && u >= 0.f && u <= 1.f;
+  }
+  __device__ __forceinline__ static void overflow(const Params& P, int row) {
+    if (threadIdx.x == 0) P.token[row] = kListLeft;
+  }
+  __device__ __forceinline__ static void none(const Params& P, int row, uint32_t status) {
+    if (threadIdx.x != 0) return;
+    P.token[row] = -1;
+    if (P.logprob) P.logprob[row] = __int_as_float(0x7FC00000);
+    if (P.support_size) P.support_size[row] = 0;
+    if (P.status) P.status[row] = status;
+  }
+  // masses: room for nk words
+  template <typename Raw>
+  __device__ __forceinline__ static void finish(const Params& P, int row, u64* sorted, u64* masses, uint32_t nk,
+                                                float vmax, float) {
+    float t = t_of(P, row), p = P.top_p ? P.top_p[row] : P.top_p_scalar, m = P.min_p ? P.min_p[row] : P.min_p_scalar;
+    if (t == 0.f) {
+      t = 1.f;
+      p = 1.f;
+      m = 0.f;
+    }
+    const double inv_t = 1.0 / static_cast<double>(t), scale = static_cast<double>(1ull << P.fx_shift);
+    auto z_of = [&](uint32_t i) {
+      const float v = KeyTraits<Raw>::decode(static_cast<uint32_t>(sorted[i] >> 32));
+      return (static_cast<double>(v) - static_cast<double>(vmax)) * inv_t;
+    };
+    for (uint32_t i = threadIdx.x; i < nk; i += kLThreads) masses[i] = __double2ull_rn(exp(z_of(i)) * scale);
+    cta_sync();
+    if (threadIdx.x >= 32) return;
+    const int lane = threadIdx.x;
+    // the first of n elements at which the running mass reaches want; sum: the mass through it
+    auto cross = [&](uint32_t n, u64 want, u64& sum) {
+      sum = 0ull;
+      for (uint32_t i0 = 0; i0 < n; i0 += 32) {
+        u64 s = i0 + lane < n ? masses[i0 + lane] : 0ull;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const u64 x = __shfl_up_sync(0xffffffffu, s, o);
+          if (lane >= o) s += x;
+        }
+        s += sum;
+        const uint32_t hit = __ballot_sync(0xffffffffu, i0 + lane < n && s >= want);
+        if (hit) {
+          const int l = __ffs(hit) - 1;
+          sum = __shfl_sync(0xffffffffu, s, l);
+          return i0 + l;
+        }
+        sum = __shfl_sync(0xffffffffu, s, 31);
+      }
+      return n - 1;
+    };
+    u64 mass;
+    uint32_t n = nk;
+    cross(n, ~0ull, mass);  // never reached: the total
+    if (p < 1.f) n = cross(nk, topp_target(p, static_cast<double>(mass)), mass) + 1u;
+    if (m > 0.f) {
+      uint32_t keep = 0u;  // the order is by mass: those kept are the first ones
+      for (uint32_t i = lane; i < n; i += 32) keep += exp(z_of(i)) >= static_cast<double>(m) ? 1u : 0u;
+      n = __reduce_add_sync(0xffffffffu, keep);
+      cross(n, ~0ull, mass);
+    }
+    u64 upto;
+    const uint32_t at = cross(n, draw_target(P.uniform[row], mass), upto);
+    if (lane == 0) {
+      P.token[row] = static_cast<int32_t>(~static_cast<uint32_t>(sorted[at]));
+      if (P.logprob) P.logprob[row] = static_cast<float>(z_of(at) - log(static_cast<double>(mass) / scale));
+      if (P.support_size) P.support_size[row] = static_cast<int32_t>(n);
+      if (P.status) P.status[row] = 0u;
+    }
+  }
+};
+
+// Wait (bounded) for a peer's release on this barrier's first phase.
+__device__ __forceinline__ void wait_cluster(uint64_t* bar) {
+  for (uint32_t i = 0; i < kWaitLimit; ++i) {
+    uint32_t ok;
+    asm volatile(
+        "{\n .reg .pred p;\n mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], 0;\n"
+        " selp.u32 %0, 1, 0, p;\n}\n"
+        : "=r"(ok)
+        : "r"(smem_addr(bar))
+        : "memory");
+    if (ok) return;
+  }
+}
+
+template <typename Raw, typename Op>
+__global__ void __launch_bounds__(kLThreads, 5) list_kernel(const __grid_constant__ typename Op::Params P, int chunk,
+                                                            int local) {
+  extern __shared__ __align__(16) unsigned char l_smem[];
+  ListStage& sh = *reinterpret_cast<ListStage*>(l_smem);
+  u64* more = reinterpret_cast<u64*>(l_smem + sizeof(ListStage));
+  Raw* buf = reinterpret_cast<Raw*>(l_smem + sizeof(ListStage) + list_more(local));
+  constexpr Raw kMaskedRaw = static_cast<Raw>(sizeof(Raw) == 2 ? 0xFF80u : 0xFF800000u);
+  cg::cluster_group cl = cg::this_cluster();
+  const int C = static_cast<int>(cl.num_blocks()), rank = static_cast<int>(cl.block_rank());
+  const int row = static_cast<int>(blockIdx.x) / C;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the general kernel's rows need not wait
+  const int k = Op::k_of(P, row);
+  if (k <= 0) return;  // not a list row: the whole cluster leaves
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const Raw* x = static_cast<const Raw*>(P.logits) + static_cast<int64_t>(row) * P.ld;
+  const int j0 = min(P.vocab, rank * chunk), j1 = min(P.vocab, j0 + chunk);
+  const int n = j1 - j0, groups = (n + 7) / 8;  // of eight elements, the last one filled up with masked ones
+  const uint32_t bytes = static_cast<uint32_t>(n / 8) * 8u * sizeof(Raw);
+  if (tid == 0) {
+    mbar_init(&sh.bar, 1);
+    mbar_init(&sh.xbar, 1);
+    mbar_init(&sh.lbar, 1);
+    mbar_init(&sh.fbar, 1);
+    for (int r = 0; r < kLMaxCluster; ++r) mbar_init(&sh.gbar[r], 1);
+    fence_barrier_init();
+    fence_proxy_async();
+    mbar_arrive_expect_tx(&sh.xbar, static_cast<uint32_t>(C * sizeof(ListPart)));
+    if (bytes) {
+      mbar_arrive_expect_tx(&sh.bar, bytes);
+      bulk_load_all(buf, x + j0, bytes, &sh.bar);
+    }
+    if (rank == 0) mbar_arrive_expect_tx(&sh.lbar, static_cast<uint32_t>(C * sizeof(ListPush)));
+    sh.mine.n = sh.bad = 0u;
+  }
+  __syncwarp();
+  asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");  // ordered by the fence above
+  for (int i = n / 8 * 8 + tid; i < groups * 8; i += kLThreads) buf[i] = i < n ? x[j0 + i] : kMaskedRaw;
+  for (int i = tid; i < kLBins; i += kLThreads) {
+    sh.bins[i] = 0u;
+    sh.least[i] = 0xFFFFFFFFu;
+  }
+  if (tid >= 64 && tid < 64 + kLPush) sh.mine.e[tid - 64] = 0ull;
+  const bool fine = Op::fine(P, row);
+  const float t = Op::t_of(P, row), c = fminf(kLog2e / t, 3e38f);
+  cta_sync();
+  if (bytes && !mbar_wait(&sh.bar, 0)) atomicOr(&sh.bad, 1u);
+  __syncwarp();
+
+  // the thread's two maxima (of its even and its odd groups), and its sum
+  uint32_t mine, top[2];
+  {
+    float m0 = -kInf, m1 = -kInf;
+    auto seen = [&](float v) {
+      const float old = m0;
+      m0 = m1;
+      m1 = max_nan(old, v);
+    };
+    if constexpr (Op::kSum) {
+      float m, z;
+      slice_sum(buf, tid, groups, kLThreads, c, m, z, seen);
+      const float wm = warp_max_nan(m);
+      z = warp_sum(z != 0.f ? z * ex2((m - wm) * c) : 0.f);
+      if (lane == 0) sh.red[warp] = make_float2(wm, z);
+    } else {
+      for (int g = tid; g < groups; g += kLThreads) {
+        Eight<Raw> v;
+        v.load(buf + g * 8);
+        seen(max8(v));
+      }
+    }
+    const bool nan = m0 != m0 || m1 != m1;
+    top[0] = ListKey<Raw>::of(m0);
+    top[1] = ListKey<Raw>::of(m1);
+    mine = nan ? 0xFFFFFFFFu : max(top[0], top[1]);
+  }
+  {
+    uint32_t low = 0xFFFFFFFFu;
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      if (top[i] > ListKey<Raw>::kMasked) low = min(low, top[i]);
+    const uint32_t wmax = __reduce_max_sync(0xffffffffu, mine), wmin = __reduce_min_sync(0xffffffffu, low);
+    if (lane == 0) {
+      sh.rmax[warp] = wmax;
+      sh.rmin[warp] = wmin;
+    }
+  }
+  cta_sync();
+  const uint32_t bmax = __reduce_max_sync(0xffffffffu, lane < kLWarps ? sh.rmax[lane] : 0u);
+  const uint32_t bmin = __reduce_min_sync(0xffffffffu, lane < kLWarps ? sh.rmin[lane] : 0xFFFFFFFFu);
+  if (bmax < KeyTraits<Raw>::kInfKey && bmax > ListKey<Raw>::kMasked) {
+    // bins over the maxima's range, at most 100 below the largest (masks by a huge negative value)
+    const float high = KeyTraits<Raw>::decode(bmax), range = fminf(high - KeyTraits<Raw>::decode(bmin), 100.f);
+    const float per = range > 0.f ? fminf((kLBins - 1) / range, 1e30f) : 0.f;
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      if (top[i] > ListKey<Raw>::kMasked) {
+        const int b = static_cast<int>(fminf((high - KeyTraits<Raw>::decode(top[i])) * per, kLBins - 1.f));
+        atomicAdd(&sh.bins[b], 1u);
+        atomicMin(&sh.least[b], top[i]);
+      }
+  }
+  cta_sync();
+  asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
+  if (warp == 0) {
+    ListPart part{};
+    uint32_t cnt[kLBins / 32], sum = 0u;
+#pragma unroll
+    for (int i = 0; i < kLBins / 32; ++i) {
+      cnt[i] = sh.bins[lane * (kLBins / 32) + i];
+      sum += cnt[i];
+    }
+    uint32_t upto = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint32_t a = __shfl_up_sync(0xffffffffu, upto, o);
+      if (lane >= o) upto += a;
+    }
+    const int bk = bin_reaching(upto, sum, cnt, static_cast<uint32_t>(k));
+    const int bs = bin_reaching(upto, sum, cnt, static_cast<uint32_t>((k + C - 1) / C));
+    part.kth = bk < 0 ? 0u : sh.least[bk];
+    part.share = bs < 0 ? 0u : sh.least[bs];
+    part.kmax = bmax;
+    if (sh.bad) part.kmax = 0xFFFFFFFFu;
+    if constexpr (Op::kSum) {
+      const float2 r = lane < kLWarps ? sh.red[lane] : make_float2(-kInf, 0.f);
+      part.m = warp_max_nan(r.x);
+      part.z = warp_sum(r.y != 0.f ? r.y * ex2((r.x - part.m) * c) : 0.f);
+    }
+    if (lane < C)
+      push_words<sizeof(ListPart) / 16>(peer_addr(&sh.parts[rank], lane), peer_addr(&sh.xbar, lane), &part);
+  }
+  const bool got = mbar_wait(&sh.xbar, 0);
+  __syncwarp();
+  const ListPart p = lane < C ? sh.parts[lane] : ListPart{0u, 0u, 0xFFFFFFFFu, -kInf, 0.f, {0u, 0u, 0u}};
+  const uint32_t kmax = __reduce_max_sync(0xffffffffu, p.kmax);
+  const uint32_t floor_key = max(max(__reduce_max_sync(0xffffffffu, p.kth), __reduce_min_sync(0xffffffffu, p.share)),
+                                 ListKey<Raw>::kMasked + 1u);
+  const bool finite = kmax < KeyTraits<Raw>::kInfKey && got, empty = finite && kmax <= ListKey<Raw>::kMasked;
+  if (!finite || !fine || empty) {  // the same in every CTA
+    if (rank == 0)
+      Op::none(P, row, (finite ? 0u : VS_ROW_NONFINITE_INPUT) | (fine ? 0u : VS_ROW_BAD_PARAM) |
+                           (empty ? VS_ROW_EMPTY_SUPPORT : 0u) | (got ? 0u : VS_ROW_DEVICE_TIMEOUT));
+    return;
+  }
+  const float vmax = KeyTraits<Raw>::decode(kmax);
+
+  // list the elements from the floor up
+  if (max(top[0], top[1]) >= floor_key) {
+    const float low = KeyTraits<Raw>::decode(floor_key);
+    for (int g = tid; g < groups; g += kLThreads) {
+      Eight<Raw> v;
+      v.load(buf + g * 8);
+      if (max8(v) < low) continue;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float e = value_of(v.e[i]);
+        if (e >= low) {
+          const uint32_t at = atomicAdd(&sh.mine.n, 1u);
+          const u64 w = static_cast<u64>(ListKey<Raw>::of(e)) << 32 | static_cast<uint32_t>(~(j0 + g * 8 + i));
+          if (at < kLPush)
+            sh.mine.e[at] = w;
+          else if (at < static_cast<uint32_t>(local))
+            more[at - kLPush] = w;
+        }
+      }
+    }
+  }
+  cta_sync();
+  if (warp == 0)
+    push_words<1>(peer_addr(reinterpret_cast<char*>(&sh.pushed[rank]) + 16 * lane, 0), peer_addr(&sh.lbar, 0),
+                  reinterpret_cast<const char*>(&sh.mine) + 16 * lane);
+  if (tid == 0 && rank != 0 && sh.mine.n > static_cast<uint32_t>(kLPush))
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(peer_addr(&sh.gbar[rank], 0)) : "memory");
+  if (rank != 0) {
+    // leave, or stay until the leader has fetched what was not pushed
+    if (sh.mine.n > static_cast<uint32_t>(kLPush)) mbar_wait(&sh.fbar, 0);
+    return;
+  }
+  const bool all = mbar_wait(&sh.lbar, 0);
+  __syncwarp();
+  u64* list = reinterpret_cast<u64*>(buf);
+  uint32_t cnt = lane < C && all ? sh.pushed[lane].n : 0u, upto = cnt;
+#pragma unroll
+  for (int o = 1; o < kLMaxCluster; o <<= 1) {
+    const uint32_t a = __shfl_up_sync(0xffffffffu, upto, o);
+    if (lane >= o) upto += a;
+  }
+  const uint32_t total = __shfl_sync(0xffffffffu, upto, C - 1);
+  const bool over = !all || total > static_cast<uint32_t>(kLTotal) ||
+                    __any_sync(0xffffffffu, cnt > static_cast<uint32_t>(local));
+  for (int r = warp; r < C; r += kLWarps) {  // the warps share the peers' lists
+    const uint32_t nc = __shfl_sync(0xffffffffu, cnt, r), at = __shfl_sync(0xffffffffu, upto, r) - nc;
+    // also when nothing is read: this CTA must not leave before the peer's arrival is in
+    if (r != 0 && nc > static_cast<uint32_t>(kLPush)) wait_cluster(&sh.gbar[r]);
+    if (!over) {
+      for (uint32_t i = lane; i < min(nc, static_cast<uint32_t>(kLPush)); i += 32) list[at + i] = sh.pushed[r].e[i];
+      const u64* rest = cl.map_shared_rank(more, r);
+      for (uint32_t i = kLPush + lane; i < nc; i += 32) list[at + i] = rest[i - kLPush];
+    }
+    __syncwarp();
+    if (r != 0 && lane == 0 && nc > static_cast<uint32_t>(kLPush))
+      asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(peer_addr(&sh.fbar, r)) : "memory");
+  }
+  cta_sync();
+  if (over) {
+    Op::overflow(P, row);
+    return;
+  }
+  const uint32_t nk = min(static_cast<uint32_t>(k), total);
+  u64* spare = list + list_total(C, local);
+  u64* sorted = list_sort(list, spare, total, nk);
+  float z = 0.f;
+  if constexpr (Op::kSum)
+    z = warp_sum(lane < C && p.z != 0.f ? p.z * ex2((p.m - vmax) * c) : 0.f);
+  Op::template finish<Raw>(P, row, sorted, sorted == list ? spare : list, nk, vmax, z);
+}
+
+template <typename Raw, typename Op>
+cudaError_t launch_list(const typename Op::Params& P, cudaStream_t s, bool* done) {
+  int c = stage_cluster_size(P.rows, P.vocab, sizeof(Raw));
+  *done = c != 0;
+  // wide lists: a CTA's share of k stays well below its 512 maxima and its list
+  while (c != 0 && c < kLMaxCluster && Op::most(P) > 128 * c) c *= 2;
+  if (c == 0) return cudaSuccess;
+  const int chunk = ((P.vocab + c - 1) / c + 31) / 32 * 32;
+  const int local = list_local(std::max(Op::most(P), 1));
+  const size_t smem = sizeof(ListStage) + list_room(c, local, static_cast<size_t>(chunk) * sizeof(Raw));
+  cudaError_t e = cudaFuncSetAttribute(list_kernel<Raw, Op>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       static_cast<int>(smem));
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>(P.rows) * c);
+  cfg.blockDim = dim3(kLThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = c;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, list_kernel<Raw, Op>, P, chunk, local);
+}
+
+}  // namespace
+
+cudaError_t launch_sample_list(const SampleParams& P, vs_dtype dtype, cudaStream_t s, bool* done) {
+  return dtype == VS_BF16 ? launch_list<uint16_t, SampleOp>(P, s, done) : launch_list<uint32_t, SampleOp>(P, s, done);
+}
+
+cudaError_t launch_topk_list(const TopkParams& P, vs_dtype dtype, cudaStream_t s, bool* done) {
+  return dtype == VS_BF16 ? launch_list<uint16_t, TopkOp>(P, s, done) : launch_list<uint32_t, TopkOp>(P, s, done);
+}
+
+}  // namespace vs

@@ -5,6 +5,8 @@
 #include <cuda_bf16.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "common.cuh"
 
 namespace vs {
@@ -92,8 +94,14 @@ __device__ __forceinline__ void push_words(uint32_t dst, uint32_t bar, const voi
 // multiply-add per exponent, the rounding of m c put back after.  Masked
 // first groups, far larger values later, and l c that overflows take the
 // thread's maximum and the differences first.  A NaN or +inf comes out as m.
-template <typename Raw>
-__device__ __forceinline__ void slice_sum(const Raw* buf, int g0, int groups, int step, float c, float& m, float& z) {
+// seen(group's maximum) runs once for every group when Seen is not empty.
+struct SeenNone {
+  __device__ __forceinline__ void operator()(float) const {}
+};
+template <typename Raw, typename Seen = SeenNone>
+__device__ __forceinline__ void slice_sum(const Raw* buf, int g0, int groups, int step, float c, float& m, float& z,
+                                          Seen&& seen = Seen{}) {
+  constexpr bool kSeen = !std::is_same_v<std::decay_t<Seen>, SeenNone>;
   m = -kInf;
   z = 0.f;
   if (g0 >= groups) return;
@@ -103,12 +111,20 @@ __device__ __forceinline__ void slice_sum(const Raw* buf, int g0, int groups, in
     m = max8(v);
   }
   const float mc = __fmul_rn(m, c);
-  if (fabsf(mc) < 1e37f) {
+  const bool direct = fabsf(mc) < 1e37f;
+  if (kSeen && !direct)
+    for (int g = g0; g < groups; g += step) {
+      Eight<Raw> v;
+      v.load(buf + g * 8);
+      seen(max8(v));
+    }
+  if (direct) {
     const f32x2 c2 = pack2(c, c), m2 = pack2(-mc, -mc);
     f32x2 z2 = pack2(0.f, 0.f), y2 = pack2(0.f, 0.f);
     for (int g = g0; g < groups; g += step) {
       Eight<Raw> v;
       v.load(buf + g * 8);
+      if (kSeen) seen(max8(v));
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         float a, b;

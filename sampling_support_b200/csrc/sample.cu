@@ -6,16 +6,14 @@
 //   n_m = the number of tokens with w >= min_p;  the support is the first
 //   n = min(n_k, n_p, n_m) tokens;
 //   token = the first i with C_i > u C_n,  logprob = log(w_i / C_n).
+#include <algorithm>
+
 #include "internal.h"
 #include "row_select.cuh"
 
 namespace vs {
 
 namespace {
-
-// Largest top-k taken through the list of candidates above a floor (half of
-// the threads' 1,024 maxima: beyond it the floor is far below the k-th).
-constexpr int kListTopK = 512;
 
 __device__ __forceinline__ void write_none(const SampleParams& P, int row, uint32_t status) {
   P.token[row] = -1;
@@ -31,19 +29,11 @@ __device__ __forceinline__ void write_row(const SampleParams& P, int row, double
   if (P.status) P.status[row] = 0u;
 }
 
-// The running mass that the row's number asks for: the first integer above
-// u * mass, at most the mass itself (u = 1 takes the last token).
-__device__ __forceinline__ u64 draw_target(float u, u64 mass) {
-  const double x = floor(static_cast<double>(u) * static_cast<double>(mass));
-  const u64 t = x >= static_cast<double>(mass) ? mass : static_cast<u64>(x) + 1ull;
-  return t < mass ? t : mass;
-}
-
 // Leader: the support's cut and the drawn token from a list that holds at
 // least the first nk tokens of the row.  The block sorts and takes the masses;
 // its first warp decides.
 template <typename Raw>
-__device__ __forceinline__ void draw_from_list(const SampleParams& P, int row, const Settings& s, uint32_t n_list) {
+__device__ __noinline__ void draw_from_list(const SampleParams& P, int row, const Settings& s, uint32_t n_list) {
   RsShared& sh = rs_shared();
   const RsMass M = sh.M;
   const uint32_t nk = min(static_cast<uint32_t>(s.k), n_list);
@@ -426,9 +416,8 @@ __device__ __forceinline__ bool draw_by_value(const SampleParams& P, int row, co
 }
 
 template <typename Raw>
-__global__ void __launch_bounds__(kRsThreads, 1) sample_kernel(SampleParams P) {
+__device__ __forceinline__ void sample_row(const SampleParams& P, int row) {
   RsRow<Raw> R;
-  const int row = static_cast<int>(blockIdx.x / cg::this_cluster().num_blocks());
   R.init(P.logits, row, P.ld, P.vocab);
   const bool lead = R.rank == 0 && threadIdx.x == 0;
 
@@ -445,8 +434,8 @@ __global__ void __launch_bounds__(kRsThreads, 1) sample_kernel(SampleParams P) {
     s.p = 1.f;
     s.m = 0.f;
   }
-  const bool listed = s.k > 0 && s.k < P.vocab && s.k <= kListTopK;
-  bool by_value = sizeof(Raw) == 2 && fine && !listed, by_list = listed;
+  bool by_list = !P.lists && sample_list_k(P.vocab, s.t, s.k) > 0;
+  bool by_value = sizeof(Raw) == 2 && fine && !by_list;
   for (;;) {
     if constexpr (sizeof(Raw) == 2) {
       if (by_value && draw_by_value(P, row, s, R)) return;
@@ -479,6 +468,40 @@ __global__ void __launch_bounds__(kRsThreads, 1) sample_kernel(SampleParams P) {
   }
 }
 
+template <typename Raw>
+__device__ __noinline__ void sample_row_apart(const SampleParams& P, int row) {
+  sample_row<Raw>(P, row);
+}
+
+__device__ __forceinline__ bool is_list_row(const SampleParams& P, int row) {
+  return P.lists && sample_list_k(P.vocab, P.temperature ? P.temperature[row] : P.temperature_scalar,
+                                  P.top_k ? P.top_k[row] : P.top_k_scalar) > 0;
+}
+
+// One cluster per row.  Of the rows that went through the list kernel only
+// those it has left.
+template <typename Raw>
+__global__ void __launch_bounds__(kRsThreads, 1) sample_kernel(const __grid_constant__ SampleParams P) {
+  const int row = static_cast<int>(blockIdx.x / cg::this_cluster().num_blocks());
+  const bool listed = is_list_row(P, row);
+  // the list kernel's answers; and nothing after this kernel may start before that one is done
+  if (listed) asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (!listed || *reinterpret_cast<volatile int32_t*>(P.token + row) == kListLeft) sample_row<Raw>(P, row);
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
+// A call whose rows all went through the list kernel: a few CTAs look after the
+// rows it has left.
+template <typename Raw>
+__global__ void __launch_bounds__(kRsThreads, 1) sample_rest_kernel(const __grid_constant__ SampleParams P) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  for (int row = blockIdx.x; row < P.rows; row += gridDim.x) {
+    if (*reinterpret_cast<volatile int32_t*>(P.token + row) != kListLeft) continue;
+    sample_row_apart<Raw>(P, row);
+    cta_sync();  // the shared memory goes to another row
+  }
+}
+
 }  // namespace
 
 // Cluster size for `rows` rows of `vocab` elements: as many CTAs per row as
@@ -489,30 +512,50 @@ int row_cluster_size(int rows, int vocab) {
   return c;
 }
 
+// `behind`: the call's list kernel precedes; the grid may start beside its tail
+// (and waits for it where it reads what it wrote).
 template <typename K, typename Params>
-static cudaError_t launch_row(K kernel, const Params& P, cudaStream_t s) {
-  const int c = row_cluster_size(P.rows, P.vocab);
+static cudaError_t launch_rows(K kernel, const Params& P, int clusters, int c, bool behind, cudaStream_t s) {
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        static_cast<int>(sizeof(RsShared)));
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(static_cast<unsigned>(P.rows) * c);
+  cfg.gridDim = dim3(static_cast<unsigned>(clusters) * c);
   cfg.blockDim = dim3(kRsThreads);
   cfg.dynamicSmemBytes = sizeof(RsShared);
   cfg.stream = s;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = c;
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = behind ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, kernel, P);
 }
 
-cudaError_t launch_sample(const SampleParams& P, vs_dtype dtype, cudaStream_t s) {
-  return dtype == VS_BF16 ? launch_row(sample_kernel<uint16_t>, P, s)
-                          : launch_row(sample_kernel<uint32_t>, P, s);
+constexpr int kSms = 148;
+
+cudaError_t launch_sample(const SampleParams& Pin, vs_dtype dtype, cudaStream_t s) {
+  SampleParams P = Pin;
+  // whether some rows, or all, have a small top-k (per-row settings: some may)
+  const int k = P.top_k ? 0 : sample_list_k(P.vocab, 1.f, P.top_k_scalar);
+  const bool all = k > 0 || (!P.temperature && P.temperature_scalar == 0.f);
+  if (all || P.top_k || P.temperature) {
+    bool done = false;
+    const cudaError_t e = launch_sample_list(P, dtype, s, &done);
+    if (e != cudaSuccess) return e;
+    P.lists = done;
+  }
+  const bool rest = all && P.lists;  // only what the list kernel has left
+  const int c = rest ? 1 : row_cluster_size(P.rows, P.vocab), clusters = rest ? std::min(P.rows, kSms) : P.rows;
+  if (rest)
+    return dtype == VS_BF16 ? launch_rows(sample_rest_kernel<uint16_t>, P, clusters, c, true, s)
+                            : launch_rows(sample_rest_kernel<uint32_t>, P, clusters, c, true, s);
+  return dtype == VS_BF16 ? launch_rows(sample_kernel<uint16_t>, P, clusters, c, P.lists, s)
+                          : launch_rows(sample_kernel<uint32_t>, P, clusters, c, P.lists, s);
 }
 
 namespace {
@@ -579,10 +622,9 @@ __device__ __forceinline__ uint32_t topk_general(const TopkParams& P, RsRow<Raw>
 // vs_topk_logprob: the first k tokens of each row in the total order and
 // their log-probabilities  z_j - log sum_i exp z_i,  z = l / T.
 template <typename Raw>
-__global__ void __launch_bounds__(kRsThreads, 1) topk_kernel(TopkParams P) {
+__device__ __forceinline__ void topk_row(const TopkParams& P, int row) {
   RsShared& sh = rs_shared();
   RsRow<Raw> R;
-  const int row = static_cast<int>(blockIdx.x / cg::this_cluster().num_blocks());
   R.init(P.logits, row, P.ld, P.vocab);
   int32_t* ids = P.ids + static_cast<int64_t>(row) * P.out_ld;
   float* lps = P.logprob ? P.logprob + static_cast<int64_t>(row) * P.out_ld : nullptr;
@@ -652,11 +694,34 @@ __global__ void __launch_bounds__(kRsThreads, 1) topk_kernel(TopkParams P) {
   R.sync();  // the leader reads the peers' sums
 }
 
+// One cluster per row, or a few that look after the rows the list kernel has left.
+template <typename Raw>
+__global__ void __launch_bounds__(kRsThreads, 1) topk_kernel(const __grid_constant__ TopkParams P) {
+  const int C = static_cast<int>(cg::this_cluster().num_blocks());
+  const int step = static_cast<int>(gridDim.x) / C;
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // the list kernel's answers
+  for (int row = static_cast<int>(blockIdx.x) / C; row < P.rows; row += step) {
+    if (P.lists && *reinterpret_cast<volatile int32_t*>(P.ids + static_cast<int64_t>(row) * P.out_ld) != kListLeft)
+      continue;
+    topk_row<Raw>(P, row);
+    if (step < P.rows) {  // the shared memory goes to another row
+      __syncwarp();
+      cg::this_cluster().sync();
+    }
+  }
+}
+
 }  // namespace
 
-cudaError_t launch_topk(const TopkParams& P, vs_dtype dtype, cudaStream_t s) {
-  return dtype == VS_BF16 ? launch_row(topk_kernel<uint16_t>, P, s)
-                          : launch_row(topk_kernel<uint32_t>, P, s);
+cudaError_t launch_topk(const TopkParams& Pin, vs_dtype dtype, cudaStream_t s) {
+  TopkParams P = Pin;
+  bool done = false;
+  const cudaError_t e = launch_topk_list(P, dtype, s, &done);
+  if (e != cudaSuccess) return e;
+  P.lists = done;
+  const int c = done ? 1 : row_cluster_size(P.rows, P.vocab), clusters = done ? std::min(P.rows, kSms) : P.rows;
+  return dtype == VS_BF16 ? launch_rows(topk_kernel<uint16_t>, P, clusters, c, done, s)
+                          : launch_rows(topk_kernel<uint32_t>, P, clusters, c, done, s);
 }
 
 }  // namespace vs
