@@ -561,67 +561,66 @@ def support_lmhead_score(hidden, weight, targets, temperature, support_ids, want
     return out
 
 
-class _OnDevice:
-    """Runs a call on its tensors' device and stream: the launch goes to
-    `stream` (default: that device's current stream) with the device current,
-    and tensors taken to a stream other than the current one are recorded on
-    it, so that their memory is not handed out again before the call is done."""
+def _launch(fn, args, device, stream, tensors):
+    """fn(*args, stream handle) on `device`'s current stream, or on `stream`,
+    with the device current; raises on a non-zero status.  Tensors taken to a
+    stream other than the current one are recorded on it, so that their memory
+    is not handed out again before the call is done."""
+    current = torch._C._cuda_getCurrentRawStream(device.index)
+    handle = current if stream is None else stream.cuda_stream
+    if torch.cuda.current_device() == device.index:
+        rc = fn(*args, handle)
+    else:
+        with torch.cuda.device(device):
+            rc = fn(*args, handle)
+    if rc != VS_OK:
+        _check(rc)
+    if handle != current:
+        for t in tensors:
+            if t is not None:
+                t.record_stream(stream)
 
-    def __init__(self, device, stream):
-        if device.type != "cuda":
-            raise ValueError(f"tensors must be on a CUDA device, got {device}")
-        self.device, self.guard = device, torch.cuda.device(device)
-        self.stream = stream
 
-    def __enter__(self):
-        self.guard.__enter__()
-        current = torch.cuda.current_stream(self.device)
-        if self.stream is None:
-            self.stream = current
-        self.foreign = self.stream.cuda_stream != current.cuda_stream
-        return self
-
-    def __exit__(self, *exc):
-        return self.guard.__exit__(*exc)
-
-    @property
-    def handle(self):
-        return ctypes.c_void_p(self.stream.cuda_stream)
-
-    def keep(self, *tensors):
-        if self.foreign:
-            for t in tensors:
-                if isinstance(t, torch.Tensor):
-                    t.record_stream(self.stream)
+def _cuda_device(logits):
+    device = logits.device
+    if device.type != "cuda":
+        raise ValueError(f"tensors must be on a CUDA device, got {device}")
+    return device
 
 
 def _row_logits(logits, vocab):
     """(rows, vocab, row stride) of a [rows, ld] logits tensor."""
-    if logits.dim() != 2 or (logits.shape[1] > 1 and logits.stride(1) != 1):
-        raise ValueError("logits must be [rows, ld] with unit stride along the vocabulary")
+    if logits.dim() != 2:
+        raise ValueError("logits must be [rows, ld]")
     rows, width = logits.shape
+    ld, unit = logits.stride()
+    if unit != 1 and width > 1:
+        raise ValueError("logits must have unit stride along the vocabulary")
     vocab = width if vocab is None else int(vocab)
     if vocab > width:
         raise ValueError(f"vocab {vocab} exceeds the {width} columns of logits")
-    ld = logits.stride(0) if rows > 1 else max(logits.stride(0), width)
-    if rows <= 1:  # the stride of a single row says nothing: round it up to whole vectors
+    if rows <= 1:  # the stride of a single row says nothing: its width, in whole vectors
         per = 16 // logits.element_size()
-        ld = (max(ld, 1) + per - 1) // per * per
+        ld = (max(width, 1) + per - 1) // per * per
     return rows, vocab, ld
 
 
 def _check_tensor(t, name, shape, dtype, device):
-    if not isinstance(t, torch.Tensor) or t.dtype != dtype or tuple(t.shape) != tuple(shape) \
-            or t.device != device or not t.is_contiguous():
+    if not isinstance(t, torch.Tensor) or t.dtype != dtype or t.shape != shape or t.device != device \
+            or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {device}")
 
 
 def _row_setting(v, name, rows, dtype, device):
-    """(device tensor or None, scalar) of a per-row setting."""
+    """(address or None, scalar) of a per-row setting."""
     if isinstance(v, torch.Tensor):
         _check_tensor(v, name, (rows,), dtype, device)
-        return v, 0
+        return v.data_ptr(), 0
     return None, v
+
+
+def _tensors(*values):
+    return [v for v in values if isinstance(v, torch.Tensor)]
 
 
 def sample(logits, uniform, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0, vocab=None,
@@ -629,31 +628,26 @@ def sample(logits, uniform, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0, voca
     """vs_sample: one token per row of logits [rows, ld] from uniform [rows]
     (fp32 numbers in [0, 1]).  temperature (0 = greedy), top_k, top_p and min_p
     are numbers or per-row device tensors (fp32; top_k int32).  Returns
-    {"token", "logprob", "support_size", "status"}; a row without a token holds
-    -1, NaN and 0 (see the header for its status)."""
-    lib = load()
-    dev = logits.device
+    {"token", "logprob", "support_size", "status"}; a row without a token holds -1,
+    NaN and 0 (see the header for its status)."""
     rows, vocab, ld = _row_logits(logits, vocab)
+    dev = logits.device
     _check_tensor(uniform, "uniform", (rows,), torch.float32, dev)
-    t_arr, t_s = _row_setting(temperature, "temperature", rows, torch.float32, dev)
-    k_arr, k_s = _row_setting(top_k, "top_k", rows, torch.int32, dev)
-    p_arr, p_s = _row_setting(top_p, "top_p", rows, torch.float32, dev)
-    m_arr, m_s = _row_setting(min_p, "min_p", rows, torch.float32, dev)
-    a = SampleArgs(rows=rows, vocab=vocab, ld=ld, dtype=_dtype_code(logits), logits=logits.data_ptr(),
-                   temperature=None if t_arr is None else t_arr.data_ptr(), temperature_scalar=float(t_s),
-                   top_k=None if k_arr is None else k_arr.data_ptr(), top_k_scalar=int(k_s),
-                   top_p=None if p_arr is None else p_arr.data_ptr(), top_p_scalar=float(p_s),
-                   min_p=None if m_arr is None else m_arr.data_ptr(), min_p_scalar=float(m_s),
-                   uniform=uniform.data_ptr())
-    with _OnDevice(dev, stream) as on:
-        out = {"token": torch.empty(rows, dtype=torch.int32, device=dev),
-               "logprob": torch.empty(rows, dtype=torch.float32, device=dev),
-               "support_size": torch.empty(rows, dtype=torch.int32, device=dev),
-               "status": torch.empty(rows, dtype=torch.int32, device=dev)}
-        _check(lib.vs_sample(ctypes.byref(a), _p(out["token"]), _p(out["logprob"]),
-                             _p(out["support_size"]), _p(out["status"]), on.handle))
-        on.keep(logits, uniform, t_arr, k_arr, p_arr, m_arr, *out.values())
-    return out
+    t_at, t = _row_setting(temperature, "temperature", rows, torch.float32, dev)
+    k_at, k = _row_setting(top_k, "top_k", rows, torch.int32, dev)
+    p_at, p = _row_setting(top_p, "top_p", rows, torch.float32, dev)
+    m_at, m = _row_setting(min_p, "min_p", rows, torch.float32, dev)
+    dev = _cuda_device(logits)
+    a = SampleArgs(rows, vocab, ld, _dtype_code(logits), logits.data_ptr(), t_at, float(t), k_at, int(k),
+                   p_at, float(p), m_at, float(m), uniform.data_ptr())
+    token = torch.empty(rows, dtype=torch.int32, device=dev)
+    logprob = torch.empty_like(uniform)
+    size, status = torch.empty_like(token), torch.empty_like(token)
+    _launch(load().vs_sample, (ctypes.byref(a), token.data_ptr(), logprob.data_ptr(), size.data_ptr(),
+                               status.data_ptr()), dev, stream,
+            () if stream is None else _tensors(logits, uniform, temperature, top_k, top_p, min_p, token, logprob,
+                                               size, status))
+    return {"token": token, "logprob": logprob, "support_size": size, "status": status}
 
 
 def topk_logprob(logits, k, temperature=1.0, vocab=None, stream=None):
@@ -661,40 +655,38 @@ def topk_logprob(logits, k, temperature=1.0, vocab=None, stream=None):
     id ascending) and their log-probabilities over the row: {"ids" [rows, k]
     int32, "logprob" [rows, k] fp32, "status"}; -1 and -inf past a row's
     unmasked tokens."""
-    lib = load()
-    dev = logits.device
     rows, vocab, ld = _row_logits(logits, vocab)
-    t_arr, t_s = _row_setting(temperature, "temperature", rows, torch.float32, dev)
+    dev = _cuda_device(logits)
+    t_at, t = _row_setting(temperature, "temperature", rows, torch.float32, dev)
     k = int(k)
-    with _OnDevice(dev, stream) as on:
-        out = {"ids": torch.empty((rows, max(k, 0)), dtype=torch.int32, device=dev),
-               "logprob": torch.empty((rows, max(k, 0)), dtype=torch.float32, device=dev),
-               "status": torch.empty(rows, dtype=torch.int32, device=dev)}
-        _check(lib.vs_topk_logprob(rows, vocab, ld, _dtype_code(logits), _p(logits), _p(t_arr),
-                                   float(t_s), k, _p(out["ids"]), _p(out["logprob"]), k,
-                                   _p(out["status"]), on.handle))
-        on.keep(logits, t_arr, *out.values())
-    return out
+    ids = torch.empty((rows, max(k, 0)), dtype=torch.int32, device=dev)
+    logprob = torch.empty((rows, max(k, 0)), dtype=torch.float32, device=dev)
+    status = torch.empty(rows, dtype=torch.int32, device=dev)
+    _launch(load().vs_topk_logprob, (rows, vocab, ld, _dtype_code(logits), logits.data_ptr(), t_at, float(t), k,
+                                     ids.data_ptr(), logprob.data_ptr(), k, status.data_ptr()), dev, stream,
+            () if stream is None else _tensors(logits, temperature, ids, logprob, status))
+    return {"ids": ids, "logprob": logprob, "status": status}
 
 
 def _distill_args(logits, teacher_ids, teacher_logprob, temperature, tail, vocab):
-    dev = logits.device
     rows, vocab, ld = _row_logits(logits, vocab)
-    for t, name, dtype in ((teacher_ids, "teacher_ids", torch.int32),
-                           (teacher_logprob, "teacher_logprob", torch.float32)):
-        if t.dim() != 2 or t.shape[0] != rows or t.dtype != dtype or t.device != dev \
-                or (t.shape[1] > 1 and t.stride(1) != 1):
-            raise ValueError(f"{name} must be a {dtype} tensor [rows, width] on {dev}, unit stride in a row")
-    width = teacher_ids.shape[1]
-    if teacher_logprob.shape[1] != width or (rows > 1 and teacher_logprob.stride(0) != teacher_ids.stride(0)):
-        raise ValueError("teacher_ids and teacher_logprob must have the same shape and row stride")
-    t_arr, t_s = _row_setting(temperature, "temperature", rows, torch.float32, dev)
-    return DistillArgs(rows=rows, vocab=vocab, ld=ld, dtype=_dtype_code(logits), logits=logits.data_ptr(),
-                       temperature=None if t_arr is None else t_arr.data_ptr(),
-                       temperature_scalar=float(t_s), teacher_ids=teacher_ids.data_ptr(),
-                       teacher_logprob=teacher_logprob.data_ptr(), teacher_width=width,
-                       teacher_ld=max(teacher_ids.stride(0), width) if rows > 1 else width,
-                       tail=1 if tail else 0), t_arr
+    dev = logits.device
+    shape = teacher_ids.shape
+    if teacher_ids.dtype != torch.int32 or teacher_logprob.dtype != torch.float32 or teacher_ids.device != dev \
+            or teacher_logprob.device != dev:
+        raise ValueError(f"teacher_ids must be int32 and teacher_logprob float32, both on {dev}")
+    if len(shape) != 2 or shape[0] != rows or teacher_logprob.shape != shape:
+        raise ValueError("teacher_ids and teacher_logprob must be [rows, width]")
+    width = shape[1]
+    list_ld, unit = teacher_ids.stride()
+    if teacher_logprob.stride() != (list_ld, unit) or (unit != 1 and width > 1):
+        raise ValueError("teacher_ids and teacher_logprob must have the same row stride, and unit stride in a row")
+    if rows <= 1 or width == 0:
+        list_ld = width
+    t_at, t = _row_setting(temperature, "temperature", rows, torch.float32, dev)
+    _cuda_device(logits)
+    return DistillArgs(rows, vocab, ld, _dtype_code(logits), logits.data_ptr(), t_at, float(t),
+                       teacher_ids.data_ptr(), teacher_logprob.data_ptr(), width, list_ld, 1 if tail else 0)
 
 
 def _grad_like(rows, vocab, dtype, device):
@@ -713,32 +705,27 @@ def distill_fwd(logits, teacher_ids, teacher_logprob, temperature=1.0, tail=Fals
     grad_dtype (with g_loss [rows] fp32, default ones) adds "grad", the
     gradient of sum g_loss * loss, in the same pass: [rows, vocab rounded up
     to 8], columns beyond vocab unwritten."""
-    lib = load()
-    dev = logits.device
-    a, t_arr = _distill_args(logits, teacher_ids, teacher_logprob, temperature, tail, vocab)
-    rows = a.rows
+    a = _distill_args(logits, teacher_ids, teacher_logprob, temperature, tail, vocab)
+    rows, dev = a.rows, logits.device
     if g_loss is not None:
         _check_tensor(g_loss, "g_loss", (rows,), torch.float32, dev)
         if grad_dtype is None:
             raise ValueError("g_loss needs grad_dtype")
-    with _OnDevice(dev, stream) as on:
-        out = {"loss": torch.empty(rows, dtype=torch.float32, device=dev),
-               "valid": torch.empty(rows, dtype=torch.uint8, device=dev),
-               "status": torch.empty(rows, dtype=torch.int32, device=dev)}
-        if want_grad:
-            out["ctx"] = torch.empty((rows, VS_CTX_BYTES_PER_ROW), dtype=torch.uint8, device=dev)
-        if grad_dtype is not None:
-            out["grad"] = _grad_like(rows, a.vocab, grad_dtype, dev)
-        g = out.get("grad")
-        o = DistillOut(loss=out["loss"].data_ptr(), valid=out["valid"].data_ptr(),
-                       status=out["status"].data_ptr(),
-                       ctx=out["ctx"].data_ptr() if want_grad else None,
-                       g_loss=None if g_loss is None else g_loss.data_ptr(),
-                       dlogits=None if g is None else g.data_ptr(),
-                       dl_dtype=VS_BF16 if grad_dtype == torch.bfloat16 else VS_F32,
-                       grad_ld=0 if g is None else g.shape[1])
-        _check(lib.vs_distill_fwd(ctypes.byref(a), ctypes.byref(o), on.handle))
-        on.keep(logits, teacher_ids, teacher_logprob, t_arr, g_loss, *out.values())
+    loss = torch.empty(rows, dtype=torch.float32, device=dev)
+    valid = torch.empty(rows, dtype=torch.uint8, device=dev)
+    status = torch.empty(rows, dtype=torch.int32, device=dev)
+    out = {"loss": loss, "valid": valid, "status": status}
+    ctx = grad = None
+    if want_grad:
+        out["ctx"] = ctx = torch.empty((rows, VS_CTX_BYTES_PER_ROW), dtype=torch.uint8, device=dev)
+    if grad_dtype is not None:
+        out["grad"] = grad = _grad_like(rows, a.vocab, grad_dtype, dev)
+    o = DistillOut(loss.data_ptr(), valid.data_ptr(), status.data_ptr(), None if ctx is None else ctx.data_ptr(),
+                   None if g_loss is None else g_loss.data_ptr(), None if grad is None else grad.data_ptr(),
+                   VS_BF16 if grad_dtype == torch.bfloat16 else VS_F32, 0 if grad is None else grad.shape[1])
+    _launch(load().vs_distill_fwd, (ctypes.byref(a), ctypes.byref(o)), dev, stream,
+            () if stream is None else _tensors(logits, teacher_ids, teacher_logprob, temperature, g_loss,
+                                               *out.values()))
     return out
 
 
@@ -747,26 +734,24 @@ def distill_bwd(logits, teacher_ids, teacher_logprob, ctx, g_loss=None, temperat
     """vs_distill_bwd from a distill_fwd(..., want_grad=True) result's "ctx" and
     the same inputs; returns dlogits [rows, vocab rounded up to 8] (or `out`,
     overwritten or, with VS_GRAD_ACCUMULATE, added to)."""
-    lib = load()
-    dev = logits.device
-    a, t_arr = _distill_args(logits, teacher_ids, teacher_logprob, temperature, tail, vocab)
-    _check_tensor(ctx, "ctx", (a.rows, VS_CTX_BYTES_PER_ROW), torch.uint8, dev)
+    a = _distill_args(logits, teacher_ids, teacher_logprob, temperature, tail, vocab)
+    rows, dev = a.rows, logits.device
+    _check_tensor(ctx, "ctx", (rows, VS_CTX_BYTES_PER_ROW), torch.uint8, dev)
     if g_loss is not None:
-        _check_tensor(g_loss, "g_loss", (a.rows,), torch.float32, dev)
-    if out is None and mode == VS_GRAD_ACCUMULATE:
-        raise ValueError("VS_GRAD_ACCUMULATE needs out")
-    with _OnDevice(dev, stream) as on:
-        if out is None:
-            out = _grad_like(a.rows, a.vocab, grad_dtype, dev)
-        if out.dim() != 2 or out.shape[0] != a.rows or out.shape[1] < a.vocab or out.device != dev \
-                or out.dtype not in (torch.float32, torch.bfloat16) or out.stride(1) != 1:
-            raise ValueError("out must be a float32 or bfloat16 [rows, >= vocab] tensor beside logits")
-        ld = out.stride(0)
-        if a.rows == 1:
-            per = 16 // out.element_size()
-            ld = (max(ld, a.vocab) + per - 1) // per * per
-        _check(lib.vs_distill_bwd(ctypes.byref(a), _p(ctx), _p(g_loss), _p(out),
-                                  VS_BF16 if out.dtype == torch.bfloat16 else VS_F32, ld, mode,
-                                  on.handle))
-        on.keep(logits, teacher_ids, teacher_logprob, t_arr, ctx, g_loss, out)
+        _check_tensor(g_loss, "g_loss", (rows,), torch.float32, dev)
+    if out is None:
+        if mode == VS_GRAD_ACCUMULATE:
+            raise ValueError("VS_GRAD_ACCUMULATE needs out")
+        out = _grad_like(rows, a.vocab, grad_dtype, dev)
+    elif out.dim() != 2 or out.shape[0] != rows or out.shape[1] < a.vocab or out.device != dev \
+            or out.dtype not in (torch.float32, torch.bfloat16) or out.stride(1) != 1:
+        raise ValueError("out must be a float32 or bfloat16 [rows, >= vocab] tensor beside logits")
+    ld = out.stride(0)
+    if rows == 1:
+        per = 16 // out.element_size()
+        ld = (out.shape[1] + per - 1) // per * per
+    _launch(load().vs_distill_bwd,
+            (ctypes.byref(a), ctx.data_ptr(), None if g_loss is None else g_loss.data_ptr(), out.data_ptr(),
+             VS_BF16 if out.dtype == torch.bfloat16 else VS_F32, ld, mode), dev, stream,
+            () if stream is None else _tensors(logits, teacher_ids, teacher_logprob, temperature, ctx, g_loss, out))
     return out

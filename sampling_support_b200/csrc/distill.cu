@@ -704,11 +704,13 @@ static cudaError_t launch_any(DistillParams P, cudaStream_t s) {
     const int f = row_cluster_size(P.rows, P.vocab);
     P.chunk = ((P.vocab + f - 1) / f + 31) / 32 * 32;
     const size_t smem = sizeof(DistillShared) + (static_cast<size_t>(P.vocab) + 127) / 128 * 16;
-    return launch_cluster(distill_fwd_kernel<Raw, G, GRAD>, P, static_cast<unsigned>(P.rows) * f, f, kDThreads, smem, s);
+    return launch_cluster<distill_fwd_kernel<Raw, G, GRAD>>(static_cast<unsigned>(P.rows) * f, f, kDThreads, smem,
+                                                            false, s, P);
   }
   P.chunk = ((P.vocab + c - 1) / c + 31) / 32 * 32;
   const size_t smem = stage_fixed(P.width) + static_cast<size_t>(P.chunk) * sizeof(Raw);
-  return launch_cluster(distill_stage_kernel<Raw, G, GRAD>, P, static_cast<unsigned>(P.rows) * c, c, kSThreads, smem, s);
+  return launch_cluster<distill_stage_kernel<Raw, G, GRAD>>(static_cast<unsigned>(P.rows) * c, c, kSThreads, smem,
+                                                            false, s, P);
 }
 
 cudaError_t launch_distill_fwd(DistillParams P, vs_dtype dtype, vs_dtype dl_dtype, cudaStream_t s) {

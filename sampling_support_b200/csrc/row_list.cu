@@ -510,22 +510,8 @@ cudaError_t launch_list(const typename Op::Params& P, cudaStream_t s, bool* done
   const int chunk = ((P.vocab + c - 1) / c + 31) / 32 * 32;
   const int local = list_local(std::max(Op::most(P), 1));
   const size_t smem = sizeof(ListStage) + list_room(c, local, static_cast<size_t>(chunk) * sizeof(Raw));
-  cudaError_t e = cudaFuncSetAttribute(list_kernel<Raw, Op>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       static_cast<int>(smem));
-  if (e != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(static_cast<unsigned>(P.rows) * c);
-  cfg.blockDim = dim3(kLThreads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = s;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = c;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, list_kernel<Raw, Op>, P, chunk, local);
+  return launch_cluster<list_kernel<Raw, Op>>(static_cast<unsigned>(P.rows) * c, c, kLThreads, smem, false, s, P, chunk,
+                                              local);
 }
 
 }  // namespace

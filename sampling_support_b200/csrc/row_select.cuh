@@ -21,6 +21,7 @@
 
 #include "common.cuh"
 #include "internal.h"
+#include "row_stage.cuh"
 #include "select.cuh"
 
 namespace vs {
@@ -336,11 +337,6 @@ struct RsRange {
   }
 };
 
-__device__ __forceinline__ float max_nan(float a, float b) {
-  float r;
-  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
-  return r;
-}
 __device__ __forceinline__ uint32_t bmax2_nan(uint32_t a, uint32_t b) {
   const __nv_bfloat162 r = __hmax2_nan(*reinterpret_cast<const __nv_bfloat162*>(&a),
                                        *reinterpret_cast<const __nv_bfloat162*>(&b));

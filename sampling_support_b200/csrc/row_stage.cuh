@@ -5,6 +5,7 @@
 #include <cuda_bf16.h>
 #include <stdint.h>
 
+#include <atomic>
 #include <type_traits>
 
 #include "common.cuh"
@@ -168,24 +169,44 @@ inline int stage_cluster_size(int rows, int vocab, int esize) {
   return (bytes + c - 1) / c <= (200 << 10) ? c : 0;
 }
 
-// Launch `kernel` with clusters of c CTAs.
-template <typename K, typename P>
-cudaError_t launch_cluster(K kernel, const P& params, unsigned grid, int c, int threads, size_t smem, cudaStream_t s) {
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+// Lets `kernel` use `bytes` of dynamic shared memory on the current device,
+// once per device and size that grows (the attribute call costs about as much
+// host time as the launch).
+template <typename K>
+cudaError_t allow_shared(K kernel, size_t bytes, std::atomic<int> (&granted)[64]) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const int want = static_cast<int>(bytes);
+  if (dev < 64 && granted[dev].load(std::memory_order_relaxed) >= want) return cudaSuccess;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, want);
+  if (e == cudaSuccess && dev < 64) granted[dev].store(want, std::memory_order_relaxed);
+  return e;
+}
+
+// Launch `kernel` with clusters of c CTAs.  `behind`: an earlier kernel of the
+// same call precedes, and this one waits for it where it reads what it wrote.
+template <auto Kernel, typename... Args>
+cudaError_t launch_cluster(unsigned grid, int c, int threads, size_t smem, bool behind, cudaStream_t s,
+                           const Args&... args) {
+  static std::atomic<int> granted[64];
+  const cudaError_t e = allow_shared(Kernel, smem, granted);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(grid);
   cfg.blockDim = dim3(threads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = c;
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, params);
+  cfg.numAttrs = behind ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, Kernel, args...);
 }
 
 }  // namespace vs

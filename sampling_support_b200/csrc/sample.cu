@@ -10,6 +10,7 @@
 
 #include "internal.h"
 #include "row_select.cuh"
+#include "row_stage.cuh"
 
 namespace vs {
 
@@ -512,28 +513,9 @@ int row_cluster_size(int rows, int vocab) {
   return c;
 }
 
-// `behind`: the call's list kernel precedes; the grid may start beside its tail
-// (and waits for it where it reads what it wrote).
-template <typename K, typename Params>
-static cudaError_t launch_rows(K kernel, const Params& P, int clusters, int c, bool behind, cudaStream_t s) {
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       static_cast<int>(sizeof(RsShared)));
-  if (e != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(static_cast<unsigned>(clusters) * c);
-  cfg.blockDim = dim3(kRsThreads);
-  cfg.dynamicSmemBytes = sizeof(RsShared);
-  cfg.stream = s;
-  cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = c;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[1].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = behind ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, kernel, P);
+template <auto Kernel, typename Params>
+static cudaError_t launch_rows(const Params& P, int clusters, int c, bool behind, cudaStream_t s) {
+  return launch_cluster<Kernel>(static_cast<unsigned>(clusters) * c, c, kRsThreads, sizeof(RsShared), behind, s, P);
 }
 
 constexpr int kSms = 148;
@@ -552,10 +534,10 @@ cudaError_t launch_sample(const SampleParams& Pin, vs_dtype dtype, cudaStream_t 
   const bool rest = all && P.lists;  // only what the list kernel has left
   const int c = rest ? 1 : row_cluster_size(P.rows, P.vocab), clusters = rest ? std::min(P.rows, kSms) : P.rows;
   if (rest)
-    return dtype == VS_BF16 ? launch_rows(sample_rest_kernel<uint16_t>, P, clusters, c, true, s)
-                            : launch_rows(sample_rest_kernel<uint32_t>, P, clusters, c, true, s);
-  return dtype == VS_BF16 ? launch_rows(sample_kernel<uint16_t>, P, clusters, c, P.lists, s)
-                          : launch_rows(sample_kernel<uint32_t>, P, clusters, c, P.lists, s);
+    return dtype == VS_BF16 ? launch_rows<sample_rest_kernel<uint16_t>>(P, clusters, c, true, s)
+                            : launch_rows<sample_rest_kernel<uint32_t>>(P, clusters, c, true, s);
+  return dtype == VS_BF16 ? launch_rows<sample_kernel<uint16_t>>(P, clusters, c, P.lists, s)
+                          : launch_rows<sample_kernel<uint32_t>>(P, clusters, c, P.lists, s);
 }
 
 namespace {
@@ -720,8 +702,8 @@ cudaError_t launch_topk(const TopkParams& Pin, vs_dtype dtype, cudaStream_t s) {
   if (e != cudaSuccess) return e;
   P.lists = done;
   const int c = done ? 1 : row_cluster_size(P.rows, P.vocab), clusters = done ? std::min(P.rows, kSms) : P.rows;
-  return dtype == VS_BF16 ? launch_rows(topk_kernel<uint16_t>, P, clusters, c, done, s)
-                          : launch_rows(topk_kernel<uint32_t>, P, clusters, c, done, s);
+  return dtype == VS_BF16 ? launch_rows<topk_kernel<uint16_t>>(P, clusters, c, done, s)
+                          : launch_rows<topk_kernel<uint32_t>>(P, clusters, c, done, s);
 }
 
 }  // namespace vs
