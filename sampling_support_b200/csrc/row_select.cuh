@@ -36,7 +36,6 @@ constexpr int kRsMaxima = 2 * kRsThreads;  // two vector maxima per thread
 constexpr int kRsZoomBins = 1024;  // bins of a zoom into one bin, linear in the key
 constexpr int kRsCap = 4096;       // elements listed and sorted at once
 constexpr int kRsMaxCluster = 8;
-constexpr int kRsTieSteps = 64;  // 32-vector steps per warp whose matches are counted apart
 
 // Bins by the 16 leading bits of a logit (a bf16 value; an fp32 value cut off
 // towards zero), in descending order of value: one bin for each magnitude in
@@ -50,10 +49,10 @@ constexpr int kKbAll = kKbChunks * 32;
 constexpr int kKbPerLane = (kKbChunks + 31) / 32;  // chunks per lane of one warp
 
 // What the leader asks of the cluster.
-enum RsOp : uint32_t { kRsStop = 0, kRsCollect, kRsZoom, kRsSum, kRsTies, kRsLook };
+enum RsOp : uint32_t { kRsStop = 0, kRsCollect, kRsZoom, kRsSum, kRsTies };
 struct RsMsg {
-  uint32_t op, klo, khi, flag;
-  u64 a, b;
+  uint32_t op, klo, khi, flag, key, pad;
+  u64 a;
 };
 
 __device__ __forceinline__ const double* rs_tab();  // 2^(i/64), shared
@@ -115,7 +114,6 @@ struct RsDraw {
   RsBin f;           // the sums before it, its own
   uint32_t asked;    // the last request
   u64 got_cnt, got_mass;  // a kRsSum's answer
-  uint32_t middle;   // bf16: the zeros' bin may hold other values
   // the drawn element
   uint32_t key;
   int32_t id;
@@ -147,13 +145,13 @@ struct RsShared {
   uint32_t zcnt[kRsZoomBins], zlo[kRsZoomBins], zhi[kRsZoomBins];
   double tab[64];  // 2^(i/64)
   u64 sum_cnt, sum_mass;
+  u64 scan_cnt[kRsWarps], scan_mass[kRsWarps];
   uint32_t red[kRsWarps][3];
   uint32_t wcount[kRsWarps];
   float fred[kRsWarps];
   uint16_t maxima[kRsMaxima];  // leading key bits of the threads' largest vectors
-  uint32_t nlist, first;
+  uint32_t nlist;
   uint32_t x[8];  // this CTA's words of an exchange
-  u64 y[2];
   float xf[2];
   RsMsg msg[2];
   RsDraw draw;
@@ -170,8 +168,8 @@ __device__ __forceinline__ RsShared& rs_shared() {
 
 __device__ __forceinline__ const double* rs_tab() { return rs_shared().tab; }
 
-// The masses of a row with maximum v, by every thread: shared after the
-// block's next barrier.
+// The masses of a row with maximum v (or set later), by every thread: shared
+// after the block's next barrier.
 __device__ __forceinline__ void rs_set_masses(float v, float t, int shift) {
   RsShared& sh = rs_shared();
   if (threadIdx.x < 64) sh.tab[threadIdx.x] = exp2(static_cast<double>(threadIdx.x) * (1.0 / 64.0));
@@ -249,22 +247,37 @@ struct RsRow {
     return u.q;
   }
 
-  // f(vector index, its 16 bytes) over this slice's vectors, U loads in
-  // flight per thread.  The same thread gets the same vectors in every pass.
+  // f(vector index, its 16 bytes) over this slice's vectors.  The next U loads
+  // are on their way while f works on the last U (few warps share an SM here:
+  // loading and working in turn would leave each waiting for the other).  The
+  // same thread gets the same vectors in every pass.
   template <int U, typename F>
   __device__ __forceinline__ void vectors(F&& f) const {
     static_assert(VS_MAX_ROW_VOCAB / 4 / kRsThreads <= 1 << 16, "a thread's vectors count in 16 bits");
     const int full = min(v1, vocab / VEC);  // whole vectors
     const uint4* p = reinterpret_cast<const uint4*>(row);
     int v = v0 + static_cast<int>(threadIdx.x);
-    for (; v + (U - 1) * kRsThreads < full; v += U * kRsThreads) {
+    const int batches = max(0, full - v0) / (U * kRsThreads);  // complete for every thread: no predicates
+    if (batches > 0) {
       uint4 q[U];
 #pragma unroll
       for (int i = 0; i < U; ++i) q[i] = p[v + i * kRsThreads];
+#pragma unroll 1
+      for (int k = 1; k < batches; ++k) {
+        uint4 cur[U];
+#pragma unroll
+        for (int i = 0; i < U; ++i) cur[i] = q[i];
+#pragma unroll
+        for (int i = 0; i < U; ++i) q[i] = p[v + (U + i) * kRsThreads];
+#pragma unroll
+        for (int i = 0; i < U; ++i) f(v + i * kRsThreads, cur[i]);
+        v += U * kRsThreads;
+      }
 #pragma unroll
       for (int i = 0; i < U; ++i) f(v + i * kRsThreads, q[i]);
+      v += U * kRsThreads;
     }
-    // the rest, its loads together too
+#pragma unroll 1
     for (; v < full; v += 4 * kRsThreads) {
       uint4 q[4];
 #pragma unroll
@@ -489,7 +502,7 @@ __device__ __noinline__ uint32_t rs_collect(bool top, uint32_t klo, uint32_t khi
   const uint32_t lead = sizeof(Raw) == 2 ? klo : klo >> 16;
   const uint4 mine = top ? sh.top[threadIdx.x] : make_uint4(0u, 0u, 0u, 0xFFFFFFFFu);
   if (mine.w >> 16 >= lead) {
-    R.template vectors<16>(take);
+    R.template vectors<8>(take);
   } else {
     const uint32_t t[3] = {mine.x, mine.y, mine.z};
 #pragma unroll
@@ -700,16 +713,13 @@ __device__ __forceinline__ void kb_reduce(const RsRow<Raw>& R, uint32_t* cnt, ui
 }
 
 // Counts of a row's values: one shared atomic per element.  A bf16 row's
-// masked tokens are in the last bin too (those past the vocabulary among them);
-// sh.y[0] counts them in this CTA's slice, sh.y[1] is not zero when there is a
-// NaN with its sign set there (the other NaNs are in bin 0).
+// masked tokens are in the last bin too (those past the vocabulary among
+// them), and so are NaNs with their sign set (the others are in bin 0).
 template <typename Raw>
 __device__ __noinline__ void kb_count() {
   RsShared& sh = rs_shared();
   const RsRow<Raw> R = RsRow<Raw>::get();
-  if (threadIdx.x == 0) sh.y[0] = sh.y[1] = 0ull;
   kb_clear<false>(sh);
-  uint32_t masked2 = 0u, top2 = 0u;
   const uint32_t base = smem_addr(sh.cnt);
   auto inc = [&](uint32_t b) { asm volatile("red.shared.add.u32 [%0], 1;" ::"r"(base + (b << 2)) : "memory"); };
   R.template vectors<8>([&](int, const uint4& q) {
@@ -720,21 +730,11 @@ __device__ __noinline__ void kb_count() {
         const uint32_t t = kb_pair(w[i]);
         inc(t & 0xFFFFu);
         inc(t >> 16);
-        constexpr uint32_t kMasked2 = 0xFF80FF80u;
-        const uint32_t is = __heq2_mask(*reinterpret_cast<const __nv_bfloat162*>(&w[i]),
-                                        *reinterpret_cast<const __nv_bfloat162*>(&kMasked2));
-        asm("add.u16x2 %0, %1, %2;" : "=r"(masked2) : "r"(masked2), "r"(is));  // each half counts down
-        asm("max.u16x2 %0, %1, %2;" : "=r"(top2) : "r"(top2), "r"(w[i]));
       } else if (w[i] != RsRow<Raw>::kMaskedRaw) {
         inc(static_cast<uint32_t>(kb_of(w[i])));
       }
     }
   });
-  if constexpr (sizeof(Raw) == 2) {
-    const uint32_t n = (0u - masked2 & 0xFFFFu) + (0u - (masked2 >> 16) & 0xFFFFu);
-    if (n) atomicAdd(&sh.y[0], static_cast<u64>(n));
-    if ((top2 & 0xFFFFu) > 0xFF80u || (top2 >> 16) > 0xFF80u) atomicOr(&sh.y[1], 1ull);
-  }
   kb_reduce<Raw, false>(R, sh.cnt, nullptr, nullptr, kKbAll);
 }
 
@@ -768,7 +768,7 @@ __device__ __noinline__ void kb_masses() {
   const RsRow<Raw> R = RsRow<Raw>::get();
   kb_clear<true>(sh);
   const RsMass M = sh.M;
-  R.template each<4>([&](int, const auto& r) {
+  R.template each<2>([&](int, const auto& r) {
     int b[RsRow<Raw>::VEC];
     u64 w[RsRow<Raw>::VEC];
 #pragma unroll
@@ -811,66 +811,98 @@ __device__ __noinline__ void rs_zoom(uint32_t klo, uint32_t khi, int shift) {
 }
 
 // Leader, whole block: running sums of counts and masses before each chunk of
-// 32 bins.  ONE: a bin holds one value, its mass is count * w and w is
-// computed here.  Ends with a block barrier.
+// 32 bins.  ONE: a bin holds one value, its mass is count * w and w is computed
+// here; the row's maximum is the first bin's value (sh.M.vmax is set; false:
+// there is none).  Ends with a block barrier.
 template <typename Raw, bool ONE>
-__device__ __noinline__ void kb_chunks() {
+__device__ __noinline__ bool kb_chunks() {
   RsShared& sh = rs_shared();
-  const RsMass M = sh.M;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-#pragma unroll 2
-  for (int ch = warp; ch < 32 * kKbPerLane; ch += kRsWarps) {
-    uint32_t c = 0u;
-    u64 m = 0ull;
-    if (ch < kKbChunks) {
-      const int b = ch * 32 + lane;
-      const uint32_t n = sh.cnt[b];
-      if (__any_sync(0xffffffffu, n != 0u)) {
-        if (n) {
-          if (ONE) {
-            uint32_t klo, khi;
-            kb_keys<Raw>(b, klo, khi);
-            if (b == static_cast<int>(kKbSpan)) khi = KeyTraits<Raw>::kBits == 16 ? 0x7FFFu : 0x7FFFFFFFu;  // zero
-            const u64 w = M.fixed(KeyTraits<Raw>::decode(khi));
-            sh.w[b] = w;
-            m = w * n;
-          } else {
-            m = (static_cast<u64>(sh.hi[b]) << 32) + sh.lo[b];
-          }
-        }
-        c = __reduce_add_sync(0xffffffffu, n);
-        m = rs_warp_sum(m);
-      }
+  constexpr int N = (32 * kKbPerLane + kRsWarps - 1) / kRsWarps;  // this warp's chunks: warp, warp + kRsWarps, ..
+  static_assert(N <= 32, "one bit per chunk");
+  uint32_t full = 0u;
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const int ch = warp + i * kRsWarps;
+    const uint32_t n = ch < kKbChunks ? sh.cnt[ch * 32 + lane] : 0u;
+    full |= __any_sync(0xffffffffu, n != 0u) ? 1u << i : 0u;
+  }
+  if (lane < N && !(full >> lane & 1u)) {
+    const int ch = warp + lane * kRsWarps;
+    if (ch < 32 * kKbPerLane) sh.run_cnt[ch + 1] = sh.run_mass[ch + 1] = 0ull;
+  }
+  RsMass M = sh.M;
+  if (ONE) {
+    if (lane == 0) sh.red[warp][0] = full ? static_cast<uint32_t>(warp + (__ffs(full) - 1) * kRsWarps) : 0xFFFFFFFFu;
+    cta_sync();
+    const uint32_t first = __reduce_min_sync(0xffffffffu, lane < kRsWarps ? sh.red[lane][0] : 0xFFFFFFFFu);
+    if (first == 0xFFFFFFFFu) return false;
+    const int b = static_cast<int>(first) * 32 + __ffs(__ballot_sync(0xffffffffu, sh.cnt[first * 32 + lane] != 0u)) - 1;
+    uint32_t klo, khi;
+    kb_keys<Raw>(b, klo, khi);
+    if (b == static_cast<int>(kKbSpan)) khi = KeyTraits<Raw>::kBits == 16 ? 0x7FFFu : 0x7FFFFFFFu;  // zero
+    M.vmax = static_cast<double>(KeyTraits<Raw>::decode(khi));
+    if (threadIdx.x == 0) sh.M.vmax = M.vmax;
+  }
+  auto bin_mass = [&](int b) -> u64 {
+    if (!ONE) return (static_cast<u64>(sh.hi[b]) << 32) + sh.lo[b];
+    uint32_t klo, khi;
+    kb_keys<Raw>(b, klo, khi);
+    if (b == static_cast<int>(kKbSpan)) khi = KeyTraits<Raw>::kBits == 16 ? 0x7FFFu : 0x7FFFFFFFu;  // zero
+    return M.fixed(KeyTraits<Raw>::decode(khi));
+  };
+  while (full) {  // the non-empty ones, two at a time (their chains of fp64 operations overlap)
+    const int i = __ffs(full) - 1;
+    full &= full - 1u;
+    const int j = full ? __ffs(full) - 1 : i;
+    full &= full - 1u;
+    const int bi = (warp + i * kRsWarps) * 32 + lane, bj = (warp + j * kRsWarps) * 32 + lane;
+    const uint32_t ni = sh.cnt[bi], nj = sh.cnt[bj];
+    u64 wi = bin_mass(bi), wj = bin_mass(bj);
+    if (ONE) {
+      sh.w[bi] = wi;
+      sh.w[bj] = wj;
+      wi *= ni;
+      wj *= nj;
     }
+    const uint32_t ci = __reduce_add_sync(0xffffffffu, ni), cj = __reduce_add_sync(0xffffffffu, nj);
+    wi = rs_warp_sum(wi);
+    wj = rs_warp_sum(wj);
     if (lane == 0) {
-      sh.run_cnt[ch + 1] = c;
-      sh.run_mass[ch + 1] = m;
+      sh.run_cnt[(bi >> 5) + 1] = ci;
+      sh.run_mass[(bi >> 5) + 1] = wi;
+      sh.run_cnt[(bj >> 5) + 1] = cj;
+      sh.run_mass[(bj >> 5) + 1] = wj;
     }
   }
   cta_sync();
-  if (warp == 0) {  // running sums over the chunks: kKbPerLane consecutive ones per lane
-    u64 c = 0ull, m = 0ull;
-#pragma unroll
-    for (int i = 0; i < kKbPerLane; ++i) {
-      c += sh.run_cnt[lane * kKbPerLane + i + 1];
-      m += sh.run_mass[lane * kKbPerLane + i + 1];
-    }
-    u64 ec = rs_warp_scan(c) - c, em = rs_warp_scan(m) - m;
-    if (lane == 0) sh.run_cnt[0] = sh.run_mass[0] = 0ull;
-#pragma unroll
-    for (int i = 0; i < kKbPerLane; ++i) {
-      ec += sh.run_cnt[lane * kKbPerLane + i + 1];
-      em += sh.run_mass[lane * kKbPerLane + i + 1];
-      sh.run_cnt[lane * kKbPerLane + i + 1] = ec;
-      sh.run_mass[lane * kKbPerLane + i + 1] = em;
+  // running sums over the chunks, 32 to a warp
+  static_assert(kKbPerLane <= kRsWarps, "a warp for every 32 chunks");
+  u64 c = 0ull, m = 0ull;
+  if (warp < kKbPerLane) {
+    c = rs_warp_scan(sh.run_cnt[threadIdx.x + 1]);
+    m = rs_warp_scan(sh.run_mass[threadIdx.x + 1]);
+    if (lane == 31) {
+      sh.scan_cnt[warp] = c;
+      sh.scan_mass[warp] = m;
     }
   }
   cta_sync();
+  if (warp < kKbPerLane) {
+    c += rs_warp_sum(lane < warp ? sh.scan_cnt[lane] : 0ull);
+    m += rs_warp_sum(lane < warp ? sh.scan_mass[lane] : 0ull);
+    sh.run_cnt[threadIdx.x + 1] = c;
+    sh.run_mass[threadIdx.x + 1] = m;
+    if (threadIdx.x == 0) sh.run_cnt[0] = sh.run_mass[0] = 0ull;
+  }
+  cta_sync();
+  return true;
 }
 
 // One warp: the bin at which the running count (by_mass: mass) reaches t.
 template <bool ONE>
-__device__ __forceinline__ RsBin kb_find(const RsShared& sh, bool by_mass, u64 t) {
+__device__ __noinline__ RsBin kb_find(bool by_mass, u64 t) {
+  const RsShared& sh = rs_shared();
   const int lane = threadIdx.x & 31;
   const u64* run = by_mass ? sh.run_mass : sh.run_cnt;
   uint32_t below = 0u;  // chunks whose running sum stays below t
@@ -878,17 +910,24 @@ __device__ __forceinline__ RsBin kb_find(const RsShared& sh, bool by_mass, u64 t
   for (int i = 0; i < kKbPerLane; ++i) below += run[i * 32 + lane + 1] < t ? 1u : 0u;
   const int ch = min(static_cast<int>(__reduce_add_sync(0xffffffffu, below)), kKbChunks - 1);
   const int b = ch * 32 + lane;
-  const u64 n = sh.cnt[b];
-  const u64 m = n == 0ull ? 0ull : ONE ? sh.w[b] * n : (static_cast<u64>(sh.hi[b]) << 32) + sh.lo[b];
-  const u64 c = sh.run_cnt[ch] + rs_warp_scan(n), s = sh.run_mass[ch] + rs_warp_scan(m);
-  const uint32_t hit = __ballot_sync(0xffffffffu, by_mass ? s - m < t && t <= s : c - n < t && t <= c);
-  const int l = hit ? __ffs(hit) - 1 : 0;
+  const uint32_t n = sh.cnt[b];
+  const u64 m = n == 0u ? 0ull : ONE ? sh.w[b] * n : (static_cast<u64>(sh.hi[b]) << 32) + sh.lo[b];
   RsBin f;
+  int l;
+  if (by_mass) {
+    const u64 s = sh.run_mass[ch] + rs_warp_scan(m);
+    l = __ffs(__ballot_sync(0xffffffffu, s >= t && n != 0u) | 0x80000000u) - 1;
+    f.mass = __shfl_sync(0xffffffffu, s - m, l);
+    f.cnt = sh.run_cnt[ch] + __reduce_add_sync(0xffffffffu, lane < l ? n : 0u);
+  } else {
+    const u64 c = sh.run_cnt[ch] + rs_warp_scan(n);
+    l = __ffs(__ballot_sync(0xffffffffu, c >= t && n != 0u) | 0x80000000u) - 1;
+    f.cnt = __shfl_sync(0xffffffffu, c - n, l);
+    f.mass = sh.run_mass[ch] + rs_warp_sum(lane < l ? m : 0ull);
+  }
   f.bin = ch * 32 + l;
   f.n = __shfl_sync(0xffffffffu, n, l);
   f.m = __shfl_sync(0xffffffffu, m, l);
-  f.cnt = __shfl_sync(0xffffffffu, c, l) - f.n;
-  f.mass = __shfl_sync(0xffffffffu, s, l) - f.m;
   return f;
 }
 
@@ -956,51 +995,75 @@ __device__ __noinline__ void rs_sum(uint32_t klo, uint32_t khi) {
   R.sync();
 }
 
+// How many of a vector's elements equal a value (the same key: +0 and -0 too).
+template <typename Raw>
+struct RsEqual {
+  float v;
+  uint32_t v2;  // bf16, in both halves
+  __device__ __forceinline__ explicit RsEqual(uint32_t key) {
+    v = KeyTraits<Raw>::decode(key);
+    v2 = __byte_perm(__float_as_uint(v), 0, 0x3232);
+  }
+  __device__ __forceinline__ uint32_t count(const uint4& q) const {
+    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+    uint32_t n = 0u;
+    if constexpr (sizeof(Raw) == 4) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) n += __uint_as_float(w[i]) == v ? 1u : 0u;
+    } else {
+      uint32_t m[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        m[i] = __heq2_mask(*reinterpret_cast<const __nv_bfloat162*>(&w[i]), *reinterpret_cast<const __nv_bfloat162*>(&v2));
+      if (m[0] | m[1] | m[2] | m[3]) n = (__popc(m[0]) + __popc(m[1]) + __popc(m[2]) + __popc(m[3])) >> 4;
+    }
+    return n;
+  }
+  __device__ __forceinline__ uint32_t hits(const uint4& q) const {
+    Raw r[16 / sizeof(Raw)];
+    unpack(q, r);
+    uint32_t h = 0u;
+#pragma unroll
+    for (int i = 0; i < static_cast<int>(16 / sizeof(Raw)); ++i) h |= value_of(r[i]) == v ? 1u << i : 0u;
+    return h;
+  }
+};
+
 // f(id, index) for the elements equal to `key` whose index (their place in
 // the group in ascending id order, from 0) lies in [from, limit).  Each warp
-// counts a contiguous run of vectors in up to kRsTieSteps steps, then only
-// the steps that hold wanted indices are walked again in order.
+// counts a contiguous run of vectors in steps of U blocks of 32 vectors, then
+// only the steps that hold wanted indices are walked again in order.
 template <typename Raw, typename F>
 __device__ __forceinline__ void rs_ties(uint32_t key, u64 from, u64 limit, const F f) {
-  constexpr int VEC = RsRow<Raw>::VEC;
+  constexpr int VEC = RsRow<Raw>::VEC, U = 8;
   RsShared& sh = rs_shared();
   const RsRow<Raw> R = RsRow<Raw>::get();
   uint32_t* counts = reinterpret_cast<uint32_t*>(sh.sorted);  // [warp][step]
-  static_assert(sizeof(sh.sorted) >= sizeof(uint32_t) * kRsWarps * kRsTieSteps, "step counts fit the sorted list");
+  constexpr int kSteps = sizeof(sh.sorted) / sizeof(uint32_t) / kRsWarps;
+  static_assert(VS_MAX_ROW_VOCAB / 4 / kRsWarps <= kSteps * U * 32, "step counts fit the sorted list");
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int per = (R.v1 - R.v0 + kRsWarps - 1) / kRsWarps;
   const int a = min(R.v1, R.v0 + warp * per), b = min(R.v1, a + per);
-  const int blocks = (per + 31) / 32;                         // of 32 vectors
-  const int fold = (blocks + kRsTieSteps - 1) / kRsTieSteps;  // blocks per step
-  const int steps = (blocks + fold - 1) / max(fold, 1);
-  const int full = R.vocab / VEC;
-  const RsRange<Raw> range(key, key);
-  cta_sync();
-  for (int i = lane; i < steps; i += 32) counts[warp * kRsTieSteps + i] = 0u;
-  __syncwarp();
+  const int whole = min(b, R.vocab / VEC);  // the run's whole vectors; one partial may follow
+  const int steps = (b - a + U * 32 - 1) / (U * 32);
+  const RsEqual<Raw> equal(key);
+  const uint4* p = reinterpret_cast<const uint4*>(R.row);
   uint32_t n = 0u;
-  constexpr int U = 16;
-  for (int k = 0; k < blocks; k += U) {
+  cta_sync();  // the counts' room may still be read as a list
+  for (int s = 0; s < steps; ++s) {
+    const int v = a + s * U * 32 + lane;
     uint4 q[U];
 #pragma unroll
-    for (int i = 0; i < U; ++i) {
-      const int v = a + (k + i) * 32 + lane;
-      if (v < min(b, full)) q[i] = reinterpret_cast<const uint4*>(R.row)[v];
-    }
-    if (a + k * 32 <= full && full < min(b, a + (k + U) * 32)) {  // the partial vector lies here
+    for (int i = 0; i < U; ++i)
+      if (v + i * 32 < whole) q[i] = p[v + i * 32];
+    uint32_t c = 0u;
 #pragma unroll
-      for (int i = 0; i < U; ++i)
-        if (a + (k + i) * 32 + lane == full) q[i] = R.load(full);
-    }
-#pragma unroll
-    for (int i = 0; i < U; ++i) {
-      const uint32_t c = a + (k + i) * 32 + lane < b ? __popc(range.in(q[i])) : 0u;
-      if (__any_sync(0xffffffffu, c != 0u)) {
-        const uint32_t t = __reduce_add_sync(0xffffffffu, c);
-        n += t;
-        if (lane == 0) counts[warp * kRsTieSteps + (k + i) / fold] += t;
-      }
-    }
+    for (int i = 0; i < U; ++i)
+      if (v + i * 32 < whole) c += equal.count(q[i]);
+    if (whole < b && whole >= v && (whole - v) % 32 == 0 && (whole - v) / 32 < U) c += equal.count(R.load(whole));
+    c = __reduce_add_sync(0xffffffffu, c);
+    if (lane == 0) counts[warp * kSteps + s] = c;
+    n += c;
   }
   if (lane == 0) sh.wcount[warp] = n;
   cta_sync();
@@ -1017,26 +1080,70 @@ __device__ __forceinline__ void rs_ties(uint32_t key, u64 from, u64 limit, const
   base += __reduce_add_sync(0xffffffffu, lane < warp ? sh.wcount[lane] : 0u);
   if (base + n <= from || base >= limit) return;
   for (int s = 0; s < steps && base < limit; ++s) {
-    const uint32_t here = counts[warp * kRsTieSteps + s];
+    const uint32_t here = counts[warp * kSteps + s];
     if (here == 0u || base + here <= from) {
       base += here;
       continue;
     }
-    for (int k = s * fold; k < min(blocks, (s + 1) * fold); ++k) {
-      const int v = a + k * 32 + lane;
-      const uint32_t hits = v < b ? range.in(R.load(v)) : 0u;
+    const int v = a + s * U * 32 + lane;
+    uint32_t h[U];
+#pragma unroll
+    for (int i = 0; i < U; ++i) h[i] = v + i * 32 < b ? equal.hits(R.load(v + i * 32)) : 0u;
+#pragma unroll 1
+    for (int i = 0; i < U; ++i) {
+      uint32_t hits = 0u;
+#pragma unroll
+      for (int k = 0; k < U; ++k) hits = k == i ? h[k] : hits;
       const uint32_t c = __popc(hits);
       const uint32_t incl = rs_warp_scan(c);
       u64 at = base + incl - c;
-#pragma unroll
-      for (int i = 0; i < VEC; ++i)
-        if (hits >> i & 1u) {
-          if (at >= from && at < limit) f(v * VEC + i, at);
-          ++at;
-        }
+      for (; hits; hits &= hits - 1u) {
+        if (at >= from && at < limit) f((v + i * 32) * VEC + __ffs(hits) - 1, at);
+        ++at;
+      }
       base += __shfl_sync(0xffffffffu, incl, 31);
     }
   }
+}
+
+// Of a bf16 row's last bin: the number of masked tokens (those past the
+// vocabulary, which kb_count has counted too, among them); false when it holds
+// a NaN.
+static __device__ __noinline__ bool kb_masked(uint32_t* masked) {
+  RsShared& sh = rs_shared();
+  const RsRow<uint16_t> R = RsRow<uint16_t>::get();
+  const RsEqual<uint16_t> equal(RsRow<uint16_t>::kMaskedKey);
+  uint32_t n = 0u, top2 = 0u;
+  R.vectors<8>([&](int, const uint4& q) {
+    n += equal.count(q);
+    asm("max.u16x2 %0, %0, %1;" : "+r"(top2) : "r"(q.x));
+    asm("max.u16x2 %0, %0, %1;" : "+r"(top2) : "r"(q.y));
+    asm("max.u16x2 %0, %0, %1;" : "+r"(top2) : "r"(q.z));
+    asm("max.u16x2 %0, %0, %1;" : "+r"(top2) : "r"(q.w));
+  });
+  const uint32_t nan = (top2 & 0xFFFFu) > 0xFF80u || (top2 >> 16) > 0xFF80u ? 1u : 0u;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  n = __reduce_add_sync(0xffffffffu, n);
+  const uint32_t any = __reduce_or_sync(0xffffffffu, nan);
+  cta_sync();
+  if (lane == 0) {
+    sh.red[warp][1] = n;
+    sh.red[warp][2] = any;
+  }
+  cta_sync();
+  n = __reduce_add_sync(0xffffffffu, lane < kRsWarps ? sh.red[lane][1] : 0u);
+  uint32_t bad = __reduce_or_sync(0xffffffffu, lane < kRsWarps ? sh.red[lane][2] : 0u);
+  if (R.C > 1) {
+    if (threadIdx.x == 0) {
+      sh.x[6] = n;
+      sh.x[7] = bad;
+    }
+    R.sync();
+    n = __reduce_add_sync(0xffffffffu, R.from_peers(&sh.x[6], 0u));
+    bad = __reduce_or_sync(0xffffffffu, R.from_peers(&sh.x[7], 0u));
+  }
+  *masked = n;
+  return bad == 0u;
 }
 
 // Whether a bf16 row holds a value that is not zero but shares the zeros' bin.

@@ -91,14 +91,26 @@ __device__ __forceinline__ uint32_t first_above(const RsMass& M, float m, uint32
   return lo;
 }
 
+// The place, from 1, at which a group of tokens of mass w reaches d > 0 more:
+// ceil(d / w), from a rounded quotient (at most 2^20 and off by less than one)
+// and its corrections.
+__device__ __forceinline__ u64 place_in_group(u64 d, u64 w) {
+  u64 r = static_cast<u64>(fminf(static_cast<float>(d) / static_cast<float>(w), 2.f * VS_MAX_ROW_VOCAB));
+#pragma unroll
+  for (int i = 0; i < 3; ++i)
+    if (r * w < d) ++r;
+#pragma unroll
+  for (int i = 0; i < 3; ++i)
+    if (r > 1ull && (r - 1ull) * w >= d) --r;
+  return r;
+}
+
 // One step of the leader's first warp: takes what the last request brought,
 // goes on through the cuts (top-k, top-p, min-p, the draw) and fills the next
 // request.  Each cut names a bin from the running sums; where the bin does not
 // decide by itself, the cluster is asked to list its elements, to zoom into it
-// when they are too many, or to add up a part of it.  ONE: every bin holds one
-// value, whose tokens have one mass and follow one another in the order, so
-// the place inside it is arithmetic.
-template <typename Raw, bool ONE>
+// when they are too many, or to add up a part of it.
+template <typename Raw>
 __device__ __noinline__ void draw_step(RsMsg* out) {
   RsShared& sh = rs_shared();
   const int lane = threadIdx.x & 31;
@@ -111,7 +123,7 @@ __device__ __noinline__ void draw_step(RsMsg* out) {
   uint32_t klo = d.klo, khi = d.khi, asked = d.asked;
   RsBin f = d.f;
 
-  RsMsg q{kRsStop, 0u, 0u, 0u, 0ull, 0ull};
+  RsMsg q{kRsStop, 0u, 0u, 0u, 0u, 0u, 0ull};
   bool found = false, open = false;      // an element is known; a range is under search
   u64 cnt = 0ull, sum = 0ull, tie = 0ull;  // the sums through the element, its place in its group
   uint32_t key = 0u;
@@ -175,7 +187,6 @@ __device__ __noinline__ void draw_step(RsMsg* out) {
         int b = max(kb_one(__float_as_uint(top) >> 16), kb_one(__float_as_uint(vm) >> 16) - 2);
         for (; b < kKbBins; ++b) {
           kb_keys<Raw>(b, klo, khi);
-          if (ONE && b == static_cast<int>(kKbSpan)) klo = khi = 0x7FFFu;
           klo = min(klo, ktop);
           khi = min(khi, ktop);
           if (!(M.w(KeyTraits<Raw>::decode(klo)) >= static_cast<double>(s.m))) break;
@@ -183,17 +194,13 @@ __device__ __noinline__ void draw_step(RsMsg* out) {
         if (b == kKbBins) continue;
         const int at = (b & ~31) + lane;
         const u64 c = sh.cnt[at];
-        const u64 m = c == 0ull ? 0ull : ONE ? sh.w[at] * c : (static_cast<u64>(sh.hi[at]) << 32) + sh.lo[at];
+        const u64 m = (static_cast<u64>(sh.hi[at]) << 32) + sh.lo[at];
         f.bin = b;
         f.cnt = sh.run_cnt[b >> 5] + rs_warp_sum(at < b ? c : 0ull);
         f.mass = sh.run_mass[b >> 5] + rs_warp_sum(at < b ? m : 0ull);
         f.n = __shfl_sync(0xffffffffu, c, b & 31);
         if (f.cnt >= n) continue;
-        if (ONE && d.middle && b == static_cast<int>(kKbSpan)) {
-          q.op = kRsLook;
-          break;
-        }
-        if (f.n == 0ull || ONE || !(M.w(KeyTraits<Raw>::decode(khi)) >= static_cast<double>(s.m))) {
+        if (f.n == 0ull || !(M.w(KeyTraits<Raw>::decode(khi)) >= static_cast<double>(s.m))) {
           n = f.cnt;
           mass = f.mass;
           continue;
@@ -206,23 +213,19 @@ __device__ __noinline__ void draw_step(RsMsg* out) {
         by_mass = true;
         t = draw_target(s.u, mass);
       }
-      f = kb_find<ONE>(sh, by_mass, t);
+      f = kb_find<false>(by_mass, t);
       if (phase == 1 && f.cnt >= n) {  // not before the top-k cut
         phase = 2;
         continue;
-      }
-      if (ONE && d.middle && f.bin == static_cast<int>(kKbSpan)) {
-        q.op = kRsLook;
-        break;
       }
       kb_keys<Raw>(f.bin, klo, khi);
       open = true;
     }
     if (!found) {  // inside the range
-      if (ONE || klo == khi) {
-        key = ONE && f.bin == static_cast<int>(kKbSpan) ? 0x7FFFu : khi;
-        const u64 w = ONE ? sh.w[f.bin] : M.fixed(KeyTraits<Raw>::decode(khi));
-        tie = by_mass ? (t - f.mass + w - 1) / w : t - f.cnt;
+      if (klo == khi) {
+        key = khi;
+        const u64 w = M.fixed(KeyTraits<Raw>::decode(khi));
+        tie = by_mass ? place_in_group(t - f.mass, w) : t - f.cnt;
         cnt = f.cnt + tie;
         sum = f.mass + tie * w;
       } else if (f.n == 1ull && phase < 3) {
@@ -272,50 +275,44 @@ __device__ __noinline__ void draw_tie(uint32_t key, u64 r, int32_t* token) {
   rs_ties<Raw>(key, r - 1ull, r, [token](int id, u64) { *token = id; });
 }
 
-// The cuts and the draw from the row's bins (kb_chunks done).  False: a cut
-// fell into the zeros' bin, which may hold other values (`middle`).
-template <typename Raw, bool ONE>
-__device__ __forceinline__ bool draw_from_bins(const SampleParams& P, int row, const Settings& s, RsRow<Raw>& R,
-                                               bool middle) {
+// The cuts and the draw from the row's bins (kb_chunks done).
+template <typename Raw>
+__device__ __forceinline__ void draw_from_bins(const SampleParams& P, int row, const Settings& s, RsRow<Raw>& R) {
   RsShared& sh = rs_shared();
   if (R.rank == 0 && threadIdx.x == 0) {
     RsDraw& d = sh.draw;
     d.s = s;
     d.phase = 0;
     d.asked = kRsStop;
-    d.middle = middle;
     d.n = sh.run_cnt[32 * kKbPerLane];
     d.mass = sh.run_mass[32 * kKbPerLane];
   }
   __syncwarp();
   for (;;) {
     const RsMsg msg = R.broadcast([&](RsMsg* out) {
-      if (threadIdx.x < 32) draw_step<Raw, ONE>(out);
+      if (threadIdx.x < 32) draw_step<Raw>(out);
     });
-    if constexpr (!ONE) {
-      if (msg.op == kRsCollect) {
-        cta_sync();
-        if (threadIdx.x == 0) sh.nlist = 0u;
-        R.sync();
-        const uint32_t k = min(rs_collect<Raw>(false, msg.klo, msg.khi), static_cast<uint32_t>(kRsCap));
-        if (R.rank == 0) {
-          rs_sort(k, k);
-          rs_list_masses<Raw>(sh, k);
-        }
-        continue;
+    if (msg.op == kRsCollect) {
+      cta_sync();
+      if (threadIdx.x == 0) sh.nlist = 0u;
+      R.sync();
+      const uint32_t k = min(rs_collect<Raw>(false, msg.klo, msg.khi), static_cast<uint32_t>(kRsCap));
+      if (R.rank == 0) {
+        rs_sort(k, k);
+        rs_list_masses<Raw>(sh, k);
       }
-      if (msg.op == kRsZoom) {
-        int shift = 0;
-        while (((msg.khi - msg.klo) >> shift) >= static_cast<uint32_t>(kRsZoomBins)) ++shift;
-        rs_zoom<Raw>(msg.klo, msg.khi, shift);
-        continue;
-      }
-      if (msg.op == kRsSum) {
-        rs_sum<Raw>(msg.klo, msg.khi);
-        continue;
-      }
+      continue;
     }
-    if (ONE && msg.op == kRsLook) return false;
+    if (msg.op == kRsZoom) {
+      int shift = 0;
+      while (((msg.khi - msg.klo) >> shift) >= static_cast<uint32_t>(kRsZoomBins)) ++shift;
+      rs_zoom<Raw>(msg.klo, msg.khi, shift);
+      continue;
+    }
+    if (msg.op == kRsSum) {
+      rs_sum<Raw>(msg.klo, msg.khi);
+      continue;
+    }
     if (R.rank == 0 && threadIdx.x == 0) {
       const RsDraw& d = sh.draw;
       if (msg.op == kRsStop) P.token[row] = d.id;
@@ -326,7 +323,6 @@ __device__ __forceinline__ bool draw_from_bins(const SampleParams& P, int row, c
     break;
   }
   R.sync();  // peers may still read this CTA's words
-  return true;
 }
 
 // Any row, any type, any setting.
@@ -336,84 +332,144 @@ __device__ __forceinline__ void draw_general(const SampleParams& P, int row, con
   rs_set_masses(KeyTraits<Raw>::decode(kmax), s.t, P.fx_shift);
   kb_masses<Raw>();
   if (R.rank == 0) kb_chunks<Raw, false>();
-  draw_from_bins<Raw, false>(P, row, s, R, false);
+  draw_from_bins<Raw>(P, row, s, R);
+}
+
+// The leader's first warp: the cuts and the draw of a bf16 row from the counts
+// of its values.  A value's tokens have one mass and follow one another in the
+// order, so the place inside a bin is arithmetic.  False: a cut falls into the
+// zeros' bin, and it may hold other values (`middle`), or it weighs too much.
+static __device__ __noinline__ bool draw_by_counts(bool middle) {
+  RsShared& sh = rs_shared();
+  RsDraw& d = sh.draw;
+  const Settings s = d.s;
+  const int lane = threadIdx.x & 31;
+  u64 n = sh.run_cnt[32 * kKbPerLane], mass = sh.run_mass[32 * kKbPerLane];
+  // the zeros' bin is taken as zeros as long as no cut falls into it and its mass, off by
+  // at most 2^-24 / T of itself, moves the row's sum by less than 2^-40
+  if (middle && static_cast<double>(sh.w[kKbSpan]) * sh.cnt[kKbSpan] * 65536.0 * sh.M.inv_t > static_cast<double>(mass))
+    return false;
+  auto lost = [&](const RsBin& f) { return middle && f.bin == static_cast<int>(kKbSpan); };
+  if (s.k > 0 && static_cast<u64>(s.k) < n) {
+    n = static_cast<u64>(s.k);
+    const RsBin f = kb_find<true>(false, n);
+    if (lost(f)) return false;
+    mass = f.mass + (n - f.cnt) * sh.w[f.bin];
+  }
+  if (s.p < 1.f) {
+    const u64 t = topp_target(s.p, static_cast<double>(mass));
+    const RsBin f = kb_find<true>(true, t);
+    if (lost(f)) return false;
+    const u64 w = sh.w[f.bin], r = place_in_group(t - f.mass, w);
+    if (f.cnt + r < n) {
+      n = f.cnt + r;
+      mass = f.mass + r * w;
+    }
+  }
+  if (s.m > 0.f) {
+    // the first bin, from the maximum's on, whose value does not pass
+    const RsMass M = sh.M;
+    const float top = static_cast<float>(M.vmax);
+    const float vm = static_cast<float>(M.vmax + log(static_cast<double>(s.m)) / M.inv_t);
+    const int b0 = kb_one(__float_as_uint(top) >> 16);
+    int b = max(b0, kb_one(__float_as_uint(vm) >> 16) - 2);
+    for (; b < kKbBins; ++b) {
+      uint32_t klo, khi;
+      kb_keys<uint16_t>(b, klo, khi);
+      if (b == static_cast<int>(kKbSpan)) khi = 0x7FFFu;
+      if (b > b0 && !(M.w(KeyTraits<uint16_t>::decode(khi)) >= static_cast<double>(s.m))) break;
+    }
+    if (b < kKbBins) {
+      if (middle && (b == static_cast<int>(kKbSpan) || b == static_cast<int>(kKbSpan) + 1)) return false;
+      const int at = (b & ~31) + lane;
+      const uint32_t c = at < b ? sh.cnt[at] : 0u;
+      const u64 cnt = sh.run_cnt[b >> 5] + __reduce_add_sync(0xffffffffu, c);
+      if (cnt < n) {
+        n = cnt;
+        mass = sh.run_mass[b >> 5] + rs_warp_sum(c ? sh.w[at] * c : 0ull);
+      }
+    }
+  }
+  const u64 t = draw_target(s.u, mass);
+  const RsBin f = kb_find<true>(true, t);
+  if (lost(f)) return false;
+  if (lane == 0) {
+    uint32_t klo, khi;
+    kb_keys<uint16_t>(f.bin, klo, khi);
+    d.key = f.bin == static_cast<int>(kKbSpan) ? 0x7FFFu : khi;
+    d.t = place_in_group(t - f.mass, sh.w[f.bin]);
+    d.n = n;
+    d.mass = mass;
+  }
+  __syncwarp();
+  return true;
 }
 
 // A bf16 row from the counts of its values: one pass over the row (one shared
-// atomic per element and no exponential), and a second one from L2 that finds
-// the drawn token among those of its value.  Returns false when the row needs
-// the general path: values beyond the bins' range that matter.
+// atomic per element and no exponential), the decisions by the leader, and a
+// second pass from L2 that finds the drawn token among those of its value.
+// Returns false when the row needs the general path: values beyond the bins'
+// range that matter.
 __device__ __forceinline__ bool draw_by_value(const SampleParams& P, int row, const Settings& s, RsRow<uint16_t>& R) {
   RsShared& sh = rs_shared();
-  cta_sync();  // the geometry
+  rs_set_masses(0.f, s.t, P.fx_shift);  // the maximum follows
+  if (threadIdx.x == 0) sh.draw.s = s;
+  cta_sync();  // and the geometry
   kb_count<uint16_t>();
   const RsMsg ends = R.broadcast([&](RsMsg* m) {
     if (threadIdx.x == 0) {
       m->flag = sh.cnt[0];
       m->klo = sh.cnt[kKbSpan];
       m->khi = sh.cnt[kKbBins - 1];
-      sh.first = kKbBins;
     }
   });
   if (ends.flag) return false;  // above 2^17, +inf or NaN
   uint32_t low = ends.khi;      // unmasked values of the last bin
-  {
-    u64 masked = 0ull, nan = 0ull;
-    for (int c = 0; low && c < R.C; ++c) {
-      masked += R.peer(sh.y, c)[0];
-      nan |= R.peer(sh.y, c)[1];
-    }
-    if (nan) return false;
-    low -= static_cast<uint32_t>(masked);
+  if (low) {
+    uint32_t masked;
+    if (!kb_masked(&masked)) return false;
+    low -= masked;
+    if (R.rank == 0 && threadIdx.x == 0) sh.cnt[kKbBins - 1] = low;
+    __syncwarp();
   }
-  bool middle = ends.klo != 0u;
-  const RsMsg got = R.broadcast([&](RsMsg* msg) {
-    if (threadIdx.x == 0) sh.cnt[kKbBins - 1] = low;
-    cta_sync();
-    int first = kKbBins;
-#pragma unroll 4
-    for (int b = kKbAll - kRsThreads + static_cast<int>(threadIdx.x); b >= 0; b -= kRsThreads)
-      if (b < kKbBins && sh.cnt[b]) first = b;
-    first = static_cast<int>(__reduce_min_sync(0xffffffffu, static_cast<uint32_t>(first)));
-    if ((threadIdx.x & 31) == 0 && first < kKbBins) atomicMin(&sh.first, static_cast<uint32_t>(first));
-    cta_sync();
-    first = static_cast<int>(sh.first);
-    uint32_t flag = 0u;
-    if (first >= kKbBins) {
-      flag = 2u;  // every token masked
-    } else {
-      uint32_t klo, khi;
-      kb_keys<uint16_t>(first, klo, khi);
-      if (first == static_cast<int>(kKbSpan)) khi = 0x7FFFu;
-      rs_set_masses(KeyTraits<uint16_t>::decode(khi), s.t, P.fx_shift);
-      cta_sync();
-      if (low && sh.M.z(-131072.f) >= -46.0) flag = 1u;  // the last bin's values have masses of their own
-      if (!flag) kb_chunks<uint16_t, true>();
+  bool chunks = false, middle = ends.klo != 0u;
+  for (;;) {
+    const RsMsg got = R.broadcast([&](RsMsg* msg) {
+      uint32_t flag = 0u;
+      if (!chunks) {
+        cta_sync();
+        if (!kb_chunks<uint16_t, true>())
+          flag = 2u;  // every token masked
+        else if (low && sh.M.z(-131072.f) >= -46.0)
+          flag = 1u;  // the last bin's values have masses of their own
+      }
+      if (threadIdx.x >= 32) return;
+      if (flag == 0u && !draw_by_counts(middle)) flag = 3u;
+      if (threadIdx.x == 0) {
+        msg->flag = flag;
+        msg->key = sh.draw.key;
+        msg->a = sh.draw.t;
+      }
+      __syncwarp();
+    });
+    chunks = true;
+    if (got.flag == 1u) return false;
+    if (got.flag == 3u) {  // does the zeros' bin hold other values?
+      if (kb_tiny()) return false;
+      middle = false;
+      continue;
     }
-    if (threadIdx.x == 0) {
-      // the zeros' bin is taken as zeros as long as no cut falls into it and its mass, off by
-      // at most 2^-24 / T of itself, moves the row's sum by less than 2^-40
-      if (!flag && middle && static_cast<double>(sh.w[kKbSpan]) * sh.cnt[kKbSpan] * 65536.0 * sh.M.inv_t >
-                                 static_cast<double>(sh.run_mass[32 * kKbPerLane]))
-        flag = 3u;
-      msg->flag = flag;
+    if (R.rank == 0 && threadIdx.x == 0) {
+      if (got.flag == 2u)
+        write_none(P, row, VS_ROW_EMPTY_SUPPORT);
+      else
+        write_row(P, row, sh.M.z(KeyTraits<uint16_t>::decode(got.key)), sh.draw.mass, sh.draw.n, sh.M);
     }
-  });
-  if (got.flag == 1u) return false;
-  if (got.flag == 3u) {
-    if (kb_tiny()) return false;
-    middle = false;
-  }
-  if (got.flag == 2u) {
-    if (R.rank == 0 && threadIdx.x == 0) write_none(P, row, VS_ROW_EMPTY_SUPPORT);
-    R.sync();
+    __syncwarp();
+    if (got.flag == 0u) draw_tie<uint16_t>(got.key, got.a, P.token + row);
+    R.sync();  // peers may still read this CTA's words
     return true;
   }
-  while (!draw_from_bins<uint16_t, true>(P, row, s, R, middle)) {
-    if (kb_tiny()) return false;
-    middle = false;
-  }
-  return true;
 }
 
 template <typename Raw>
@@ -523,9 +579,11 @@ constexpr int kSms = 148;
 cudaError_t launch_sample(const SampleParams& Pin, vs_dtype dtype, cudaStream_t s) {
   SampleParams P = Pin;
   // whether some rows, or all, have a small top-k (per-row settings: some may)
+  // per-row settings of a larger batch: the list kernel would hold up the other rows for a few
+  // microseconds, and the general kernel lists as well
   const int k = P.top_k ? 0 : sample_list_k(P.vocab, 1.f, P.top_k_scalar);
   const bool all = k > 0 || (!P.temperature && P.temperature_scalar == 0.f);
-  if (all || P.top_k || P.temperature) {
+  if (all || ((P.top_k || P.temperature) && P.rows <= 16)) {
     bool done = false;
     const cudaError_t e = launch_sample_list(P, dtype, s, &done);
     if (e != cudaSuccess) return e;
@@ -561,7 +619,7 @@ __device__ __forceinline__ uint32_t topk_general(const TopkParams& P, RsRow<Raw>
     const RsMsg msg = R.broadcast([&](RsMsg* out) {
       if (threadIdx.x >= 32) return;
       if (!zoomed) {
-        f = kb_find<true>(sh, false, k);
+        f = kb_find<true>(false, k);
         kb_keys<Raw>(f.bin, klo, khi);
       } else {
         int shift = 0;
