@@ -3,7 +3,7 @@
 //
 // A cluster stages the row in its CTAs' shared memory (one bulk copy per
 // slice, so the row is read from HBM once) and finds a floor that at least k
-// elements reach: every thread's two vector maxima are elements of their own,
+// elements reach: every thread's two largest group maxima are elements of their own,
 // so a value that k of any CTA's maxima reach is a floor, and so is the smallest
 // over the CTAs of values that ceil(k / C) of theirs reach.  The elements from the floor
 // up (hardly more than k) are listed, gathered by the leader and sorted there.
@@ -331,15 +331,11 @@ __global__ void __launch_bounds__(kLThreads, 5) list_kernel(const __grid_constan
   if (bytes && !mbar_wait(&sh.bar, 0)) atomicOr(&sh.bad, 1u);
   __syncwarp();
 
-  // the thread's two maxima (of its even and its odd groups), and its sum
+  // the thread's two largest groups, and its sum
   uint32_t mine, top[2];
+  TwoMax two;
   {
-    float m0 = -kInf, m1 = -kInf;
-    auto seen = [&](float v) {
-      const float old = m0;
-      m0 = m1;
-      m1 = max_nan(old, v);
-    };
+    auto seen = [&](int g, const Eight<Raw>& v) { two.add(g, max8(v)); };
     if constexpr (Op::kSum) {
       float m, z;
       slice_sum(buf, tid, groups, kLThreads, c, m, z, seen);
@@ -350,13 +346,12 @@ __global__ void __launch_bounds__(kLThreads, 5) list_kernel(const __grid_constan
       for (int g = tid; g < groups; g += kLThreads) {
         Eight<Raw> v;
         v.load(buf + g * 8);
-        seen(max8(v));
+        seen(g, v);
       }
     }
-    const bool nan = m0 != m0 || m1 != m1;
-    top[0] = ListKey<Raw>::of(m0);
-    top[1] = ListKey<Raw>::of(m1);
-    mine = nan ? 0xFFFFFFFFu : max(top[0], top[1]);
+    top[0] = ListKey<Raw>::of(two.first);
+    top[1] = ListKey<Raw>::of(two.second);
+    mine = two.first != two.first ? 0xFFFFFFFFu : top[0];
   }
   {
     uint32_t low = 0xFFFFFFFFu;
@@ -430,23 +425,24 @@ __global__ void __launch_bounds__(kLThreads, 5) list_kernel(const __grid_constan
   const float vmax = KeyTraits<Raw>::decode(kmax);
 
   // list the elements from the floor up
-  if (max(top[0], top[1]) >= floor_key) {
+  if (top[0] >= floor_key) {
     const float low = KeyTraits<Raw>::decode(floor_key);
-    for (int g = tid; g < groups; g += kLThreads) {
+    // one group, as a rule; all of the thread's when a second one reaches the floor
+    const bool one = top[1] < floor_key;
+    for (int g = one ? two.at : tid; g < (one ? two.at + 1 : groups); g += kLThreads) {
       Eight<Raw> v;
       v.load(buf + g * 8);
-      if (max8(v) < low) continue;
+      uint32_t hits = 0u;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float e = value_of(v.e[i]);
-        if (e >= low) {
-          const uint32_t at = atomicAdd(&sh.mine.n, 1u);
-          const u64 w = static_cast<u64>(ListKey<Raw>::of(e)) << 32 | static_cast<uint32_t>(~(j0 + g * 8 + i));
-          if (at < kLPush)
-            sh.mine.e[at] = w;
-          else if (at < static_cast<uint32_t>(local))
-            more[at - kLPush] = w;
-        }
+      for (int i = 0; i < 8; ++i) hits |= value_of(v.e[i]) >= low ? 1u << i : 0u;
+      for (; hits; hits &= hits - 1u) {
+        const int i = g * 8 + __ffs(hits) - 1;
+        const uint32_t at = atomicAdd(&sh.mine.n, 1u);
+        const u64 w = static_cast<u64>(ListKey<Raw>::of(value_of(buf[i]))) << 32 | static_cast<uint32_t>(~(j0 + i));
+        if (at < kLPush)
+          sh.mine.e[at] = w;
+        else if (at < static_cast<uint32_t>(local))
+          more[at - kLPush] = w;
       }
     }
   }

@@ -76,6 +76,18 @@ __device__ __forceinline__ uint32_t peer_addr(const void* p, uint32_t rank) {
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(smem_addr(p)), "r"(rank));
   return r;
 }
+// The two largest group maxima seen (the first NaN once there is one), and
+// where the first is.
+struct TwoMax {
+  float first = -kInf, second = -kInf;
+  int at = 0;
+  __device__ __forceinline__ void add(int g, float t) {
+    at = t > first ? g : at;
+    second = fmaxf(second, fminf(first, t));
+    first = max_nan(first, t);
+  }
+};
+
 // N 16-byte words into a peer's shared memory, counted on its barrier there.
 template <int N>
 __device__ __forceinline__ void push_words(uint32_t dst, uint32_t bar, const void* src) {
@@ -95,9 +107,10 @@ __device__ __forceinline__ void push_words(uint32_t dst, uint32_t bar, const voi
 // multiply-add per exponent, the rounding of m c put back after.  Masked
 // first groups, far larger values later, and l c that overflows take the
 // thread's maximum and the differences first.  A NaN or +inf comes out as m.
-// seen(group's maximum) runs once for every group when Seen is not empty.
+// seen(g, group g) runs once for every group when it is given.
 struct SeenNone {
-  __device__ __forceinline__ void operator()(float) const {}
+  template <typename T>
+  __device__ __forceinline__ void operator()(int, const T&) const {}
 };
 template <typename Raw, typename Seen = SeenNone>
 __device__ __forceinline__ void slice_sum(const Raw* buf, int g0, int groups, int step, float c, float& m, float& z,
@@ -117,7 +130,7 @@ __device__ __forceinline__ void slice_sum(const Raw* buf, int g0, int groups, in
     for (int g = g0; g < groups; g += step) {
       Eight<Raw> v;
       v.load(buf + g * 8);
-      seen(max8(v));
+      seen(g, v);
     }
   if (direct) {
     const f32x2 c2 = pack2(c, c), m2 = pack2(-mc, -mc);
@@ -125,7 +138,7 @@ __device__ __forceinline__ void slice_sum(const Raw* buf, int g0, int groups, in
     for (int g = g0; g < groups; g += step) {
       Eight<Raw> v;
       v.load(buf + g * 8);
-      if (kSeen) seen(max8(v));
+      if (kSeen) seen(g, v);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         float a, b;
