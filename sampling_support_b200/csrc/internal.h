@@ -111,11 +111,9 @@ struct SampleParams {
   int32_t* support_size;
   uint32_t* status;
   int32_t fx_shift;  // fixed-point scale of the masses: vocab * 2^fx_shift <= 2^62
-  int32_t lists;     // the list kernel has gone through the rows with a small top-k
+  int32_t lists;     // the list kernel takes the rows with a small top-k
 };
 
-// A list row that the list kernel leaves to the general one (in token[row], ids[row, 0]).
-constexpr int32_t kListLeft = -2;
 // Largest top-k of vs_sample that is taken from a list of the row's largest
 // elements.  A greedy row is one of them.
 constexpr int kListTopK = 512;
@@ -143,7 +141,6 @@ struct TopkParams {
   float* logprob;
   uint32_t* status;
   int32_t fx_shift;
-  int32_t lists;  // as above
 };
 
 struct DistillParams {

@@ -14,8 +14,9 @@
 // latency (copy, floor, exchange, listing), so with 40 KB slices and five CTAs
 // per SM the rate is that of the slots.  No cluster barrier is waited for: the
 // floors and the first listed elements of every CTA are pushed, and a CTA
-// leaves once they are sent unless it has listed more.  Rows whose list overflows
-// (crowds of equal values) are marked and left to the general kernels.
+// leaves once they are sent unless it has listed more.  Where the list
+// overflows (crowds of equal values) the leader alone selects by digits of the
+// key from the row in L2: some passes of one CTA, for rows that are rare.
 #include <algorithm>
 
 #include "internal.h"
@@ -151,9 +152,6 @@ struct TopkOp {
     const float t = t_of(P, row);
     return t > 0.f && t < kInf;
   }
-  __device__ __forceinline__ static void overflow(const Params& P, int row) {
-    if (threadIdx.x == 0) P.ids[static_cast<int64_t>(row) * P.out_ld] = kListLeft;
-  }
   // no list: bad input, or every token masked
   __device__ __forceinline__ static void none(const Params& P, int row, uint32_t status) {
     int32_t* ids = P.ids + static_cast<int64_t>(row) * P.out_ld;
@@ -196,9 +194,6 @@ struct SampleOp {
     const float t = t_of(P, row), p = P.top_p ? P.top_p[row] : P.top_p_scalar, m = P.min_p ? P.min_p[row] : P.min_p_scalar;
     const float u = P.uniform[row];
     return t >= 0.f && t < kInf && p > 0.f && m <= 1.f && u >= 0.f && u <= 1.f;
-  }
-  __device__ __forceinline__ static void overflow(const Params& P, int row) {
-    if (threadIdx.x == 0) P.token[row] = kListLeft;
   }
   __device__ __forceinline__ static void none(const Params& P, int row, uint32_t status) {
     if (threadIdx.x != 0) return;
@@ -282,6 +277,113 @@ __device__ __forceinline__ void wait_cluster(uint64_t* bar) {
   }
 }
 
+// f(first id, eight elements, those past the vocabulary masked) over the whole
+// row in order, block by block of 8 kLThreads elements; the block's threads all
+// call f (it may hold barriers) until it returns false in all of them.
+template <typename Raw, typename F>
+__device__ __forceinline__ void whole_row(const Raw* x, int vocab, F&& f) {
+  constexpr Raw kMaskedRaw = static_cast<Raw>(sizeof(Raw) == 2 ? 0xFF80u : 0xFF800000u);
+  for (int b = 0; b < vocab; b += 8 * kLThreads) {
+    const int j = b + static_cast<int>(threadIdx.x) * 8;
+    Eight<Raw> v;
+    if (j + 8 <= vocab)
+      v.load(x + j);
+    else
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v.e[i] = j + i < vocab ? x[j + i] : kMaskedRaw;
+    if (!f(j, v)) return;
+  }
+}
+
+// The leader alone, whole block: the row's first k tokens (it has more) into
+// list, in any order.  The k-th key digit by digit, eight bits at a time, then
+// the elements above it and its first equals.
+template <typename Raw>
+__device__ __noinline__ void list_by_digits(const Raw* x, int vocab, int k, u64* list, ListStage& sh) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  uint32_t prefix = 0u, mask = 0u, need = static_cast<uint32_t>(k);
+  for (int shift = KeyTraits<Raw>::kBits - 8; shift >= 0; shift -= 8) {
+    cta_sync();
+    if (tid < 256) sh.bins[tid] = 0u;
+    cta_sync();
+    whole_row(x, vocab, [&](int, const Eight<Raw>& v) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const uint32_t key = key_of(v.e[i]);
+        if (key > ListKey<Raw>::kMasked && (key & mask) == prefix) atomicAdd(&sh.bins[key >> shift & 255u], 1u);
+      }
+      return true;
+    });
+    cta_sync();
+    // every warp: lane l holds the digits 255 - 8 l and down
+    uint32_t c[8], sum = 0u;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      c[i] = sh.bins[255 - 8 * lane - i];
+      sum += c[i];
+    }
+    uint32_t upto = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint32_t a = __shfl_up_sync(0xffffffffu, upto, o);
+      if (lane >= o) upto += a;
+    }
+    const int l = __ffs(__ballot_sync(0xffffffffu, upto >= need) | 0x80000000u) - 1;
+    uint32_t run = upto - sum, digit = 255u - 8u * lane, above = run;
+    bool done = false;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      run += c[i];
+      if (!done && run < need) {
+        above = run;
+        --digit;
+      } else {
+        done = true;
+      }
+    }
+    need -= __shfl_sync(0xffffffffu, above, l);
+    prefix |= (__shfl_sync(0xffffffffu, digit, l) & 255u) << shift;
+    mask |= 255u << shift;
+  }
+  // need: how many of the key's own elements belong
+  const uint32_t n_above = static_cast<uint32_t>(k) - need;
+  cta_sync();
+  if (tid == 0) sh.bins[0] = 0u;
+  cta_sync();
+  uint32_t taken = 0u;  // equals so far
+  whole_row(x, vocab, [&](int j, const Eight<Raw>& v) {
+    uint32_t eq = 0u;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const uint32_t key = key_of(v.e[i]);
+      if (key > prefix) {
+        const uint32_t at = atomicAdd(&sh.bins[0], 1u);
+        if (at < n_above) list[at] = static_cast<u64>(key) << 32 | static_cast<uint32_t>(~(j + i));
+      }
+      eq |= key == prefix ? 1u << i : 0u;
+    }
+    if (taken >= need) return true;  // the same in every thread
+    uint32_t before = __popc(eq);
+    const uint32_t mine = before;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint32_t a = __shfl_up_sync(0xffffffffu, before, o);
+      if (lane >= o) before += a;
+    }
+    cta_sync();
+    if (lane == 31) sh.rmax[warp] = before;
+    cta_sync();
+    const uint32_t w = lane < kLWarps ? sh.rmax[lane] : 0u;
+    const uint32_t all = __reduce_add_sync(0xffffffffu, w);
+    uint32_t at = taken + before - mine + __reduce_add_sync(0xffffffffu, lane < warp ? w : 0u);
+    for (; eq; eq &= eq - 1u, ++at)
+      if (at < need) list[n_above + at] = static_cast<u64>(prefix) << 32 | static_cast<uint32_t>(~(j + __ffs(eq) - 1));
+    taken += all;
+    return true;
+  });
+  cta_sync();
+}
+
 template <typename Raw, typename Op>
 __global__ void __launch_bounds__(kLThreads, 5) list_kernel(const __grid_constant__ typename Op::Params P, int chunk,
                                                             int local) {
@@ -293,7 +395,7 @@ __global__ void __launch_bounds__(kLThreads, 5) list_kernel(const __grid_constan
   cg::cluster_group cl = cg::this_cluster();
   const int C = static_cast<int>(cl.num_blocks()), rank = static_cast<int>(cl.block_rank());
   const int row = static_cast<int>(blockIdx.x) / C;
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the general kernel's rows need not wait
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // another kernel's rows need not wait for these
   const int k = Op::k_of(P, row);
   if (k <= 0) return;  // not a list row: the whole cluster leaves
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -466,9 +568,8 @@ __global__ void __launch_bounds__(kLThreads, 5) list_kernel(const __grid_constan
     const uint32_t a = __shfl_up_sync(0xffffffffu, upto, o);
     if (lane >= o) upto += a;
   }
-  const uint32_t total = __shfl_sync(0xffffffffu, upto, C - 1);
-  const bool over = !all || total > static_cast<uint32_t>(kLTotal) ||
-                    __any_sync(0xffffffffu, cnt > static_cast<uint32_t>(local));
+  uint32_t total = __shfl_sync(0xffffffffu, upto, C - 1);
+  const bool over = total > static_cast<uint32_t>(kLTotal) || __any_sync(0xffffffffu, cnt > static_cast<uint32_t>(local));
   for (int r = warp; r < C; r += kLWarps) {  // the warps share the peers' lists
     const uint32_t nc = __shfl_sync(0xffffffffu, cnt, r), at = __shfl_sync(0xffffffffu, upto, r) - nc;
     // also when nothing is read: this CTA must not leave before the peer's arrival is in
@@ -483,9 +584,13 @@ __global__ void __launch_bounds__(kLThreads, 5) list_kernel(const __grid_constan
       asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(peer_addr(&sh.fbar, r)) : "memory");
   }
   cta_sync();
-  if (over) {
-    Op::overflow(P, row);
+  if (!all) {
+    Op::none(P, row, VS_ROW_DEVICE_TIMEOUT);
     return;
+  }
+  if (over) {  // more elements than k
+    list_by_digits(x, P.vocab, k, list, sh);
+    total = static_cast<uint32_t>(k);
   }
   const uint32_t nk = min(static_cast<uint32_t>(k), total);
   u64* spare = list + list_total(C, local);

@@ -6,8 +6,6 @@
 //   n_m = the number of tokens with w >= min_p;  the support is the first
 //   n = min(n_k, n_p, n_m) tokens;
 //   token = the first i with C_i > u C_n,  logprob = log(w_i / C_n).
-#include <algorithm>
-
 #include "internal.h"
 #include "row_select.cuh"
 #include "row_stage.cuh"
@@ -525,38 +523,15 @@ __device__ __forceinline__ void sample_row(const SampleParams& P, int row) {
   }
 }
 
-template <typename Raw>
-__device__ __noinline__ void sample_row_apart(const SampleParams& P, int row) {
-  sample_row<Raw>(P, row);
-}
-
-__device__ __forceinline__ bool is_list_row(const SampleParams& P, int row) {
-  return P.lists && sample_list_k(P.vocab, P.temperature ? P.temperature[row] : P.temperature_scalar,
-                                  P.top_k ? P.top_k[row] : P.top_k_scalar) > 0;
-}
-
-// One cluster per row.  Of the rows that went through the list kernel only
-// those it has left.
+// One cluster per row.  A list kernel before it may have its own share of the
+// rows; nothing after this kernel may start before that one is done.
 template <typename Raw>
 __global__ void __launch_bounds__(kRsThreads, 1) sample_kernel(const __grid_constant__ SampleParams P) {
   const int row = static_cast<int>(blockIdx.x / cg::this_cluster().num_blocks());
-  const bool listed = is_list_row(P, row);
-  // the list kernel's answers; and nothing after this kernel may start before that one is done
-  if (listed) asm volatile("griddepcontrol.wait;" ::: "memory");
-  if (!listed || *reinterpret_cast<volatile int32_t*>(P.token + row) == kListLeft) sample_row<Raw>(P, row);
+  if (!P.lists || sample_list_k(P.vocab, P.temperature ? P.temperature[row] : P.temperature_scalar,
+                                P.top_k ? P.top_k[row] : P.top_k_scalar) == 0)
+    sample_row<Raw>(P, row);
   asm volatile("griddepcontrol.wait;" ::: "memory");
-}
-
-// A call whose rows all went through the list kernel: a few CTAs look after the
-// rows it has left.
-template <typename Raw>
-__global__ void __launch_bounds__(kRsThreads, 1) sample_rest_kernel(const __grid_constant__ SampleParams P) {
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  for (int row = blockIdx.x; row < P.rows; row += gridDim.x) {
-    if (*reinterpret_cast<volatile int32_t*>(P.token + row) != kListLeft) continue;
-    sample_row_apart<Raw>(P, row);
-    cta_sync();  // the shared memory goes to another row
-  }
 }
 
 }  // namespace
@@ -574,28 +549,22 @@ static cudaError_t launch_rows(const Params& P, int clusters, int c, bool behind
   return launch_cluster<Kernel>(static_cast<unsigned>(clusters) * c, c, kRsThreads, sizeof(RsShared), behind, s, P);
 }
 
-constexpr int kSms = 148;
-
 cudaError_t launch_sample(const SampleParams& Pin, vs_dtype dtype, cudaStream_t s) {
   SampleParams P = Pin;
-  // whether some rows, or all, have a small top-k (per-row settings: some may)
-  // per-row settings of a larger batch: the list kernel would hold up the other rows for a few
-  // microseconds, and the general kernel lists as well
-  const int k = P.top_k ? 0 : sample_list_k(P.vocab, 1.f, P.top_k_scalar);
-  const bool all = k > 0 || (!P.temperature && P.temperature_scalar == 0.f);
+  // Whether all rows have a small top-k, or (per-row settings) some may.  In a larger batch of the
+  // latter kind the list kernel would hold up the other rows for a few microseconds, and the
+  // general kernel lists as well.
+  const bool all = (!P.top_k && sample_list_k(P.vocab, 1.f, P.top_k_scalar) > 0) ||
+                   (!P.temperature && P.temperature_scalar == 0.f);
   if (all || ((P.top_k || P.temperature) && P.rows <= 16)) {
     bool done = false;
     const cudaError_t e = launch_sample_list(P, dtype, s, &done);
-    if (e != cudaSuccess) return e;
+    if (e != cudaSuccess || (all && done)) return e;
     P.lists = done;
   }
-  const bool rest = all && P.lists;  // only what the list kernel has left
-  const int c = rest ? 1 : row_cluster_size(P.rows, P.vocab), clusters = rest ? std::min(P.rows, kSms) : P.rows;
-  if (rest)
-    return dtype == VS_BF16 ? launch_rows<sample_rest_kernel<uint16_t>>(P, clusters, c, true, s)
-                            : launch_rows<sample_rest_kernel<uint32_t>>(P, clusters, c, true, s);
-  return dtype == VS_BF16 ? launch_rows<sample_kernel<uint16_t>>(P, clusters, c, P.lists, s)
-                          : launch_rows<sample_kernel<uint32_t>>(P, clusters, c, P.lists, s);
+  const int c = row_cluster_size(P.rows, P.vocab);
+  return dtype == VS_BF16 ? launch_rows<sample_kernel<uint16_t>>(P, P.rows, c, P.lists, s)
+                          : launch_rows<sample_kernel<uint32_t>>(P, P.rows, c, P.lists, s);
 }
 
 namespace {
@@ -734,34 +703,21 @@ __device__ __forceinline__ void topk_row(const TopkParams& P, int row) {
   R.sync();  // the leader reads the peers' sums
 }
 
-// One cluster per row, or a few that look after the rows the list kernel has left.
+// One cluster per row: vocabularies beyond the list kernel's shared memory.
 template <typename Raw>
 __global__ void __launch_bounds__(kRsThreads, 1) topk_kernel(const __grid_constant__ TopkParams P) {
-  const int C = static_cast<int>(cg::this_cluster().num_blocks());
-  const int step = static_cast<int>(gridDim.x) / C;
-  asm volatile("griddepcontrol.wait;" ::: "memory");  // the list kernel's answers
-  for (int row = static_cast<int>(blockIdx.x) / C; row < P.rows; row += step) {
-    if (P.lists && *reinterpret_cast<volatile int32_t*>(P.ids + static_cast<int64_t>(row) * P.out_ld) != kListLeft)
-      continue;
-    topk_row<Raw>(P, row);
-    if (step < P.rows) {  // the shared memory goes to another row
-      __syncwarp();
-      cg::this_cluster().sync();
-    }
-  }
+  topk_row<Raw>(P, static_cast<int>(blockIdx.x / cg::this_cluster().num_blocks()));
 }
 
 }  // namespace
 
-cudaError_t launch_topk(const TopkParams& Pin, vs_dtype dtype, cudaStream_t s) {
-  TopkParams P = Pin;
+cudaError_t launch_topk(const TopkParams& P, vs_dtype dtype, cudaStream_t s) {
   bool done = false;
   const cudaError_t e = launch_topk_list(P, dtype, s, &done);
-  if (e != cudaSuccess) return e;
-  P.lists = done;
-  const int c = done ? 1 : row_cluster_size(P.rows, P.vocab), clusters = done ? std::min(P.rows, kSms) : P.rows;
-  return dtype == VS_BF16 ? launch_rows<topk_kernel<uint16_t>>(P, clusters, c, done, s)
-                          : launch_rows<topk_kernel<uint32_t>>(P, clusters, c, done, s);
+  if (e != cudaSuccess || done) return e;
+  const int c = row_cluster_size(P.rows, P.vocab);
+  return dtype == VS_BF16 ? launch_rows<topk_kernel<uint16_t>>(P, P.rows, c, false, s)
+                          : launch_rows<topk_kernel<uint32_t>>(P, P.rows, c, false, s);
 }
 
 }  // namespace vs

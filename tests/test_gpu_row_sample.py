@@ -240,6 +240,32 @@ def test_offsets_beyond_32_bits():
     assert torch.equal(top["ids"][-4:], vsb.topk_logprob(tail, 8)["ids"])
 
 
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_largest_vocabulary(dtype):
+    """Rows that no cluster's shared memory holds, and one in between."""
+    for vocab in (1 << 20, 300_001):
+        x = logits_on("cuda", 2, vocab, dtype, seed=16)
+        for kw in (dict(top_k=100, top_p=0.9), dict(top_p=0.9), dict(), dict(min_p=0.1), dict(top_k=2000)):
+            check(x, numbers(2, 9), vocab, **kw)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("top_k", [3, 256, 300, 512])
+def test_lists_of_crowded_rows(dtype, top_k):
+    """More equal or nearly equal tokens than a list holds, cut by top-k: a
+    crowd at the top, one that the k-th token falls into, one in a single slice."""
+    rows, vocab = 4, 40_000
+    g = torch.Generator().manual_seed(top_k)
+    x = torch.randn((rows, vocab), generator=g)
+    x[0] = 2.0
+    x[0, ::7] = 2.0 - 1e-3
+    x[1, 5000:9000] = 6.0
+    x[1, 100:100 + top_k // 2] = 7.0
+    x[2] = torch.arange(vocab) % 3
+    x[3, :1500] = 9.0 + torch.arange(1500) % 5
+    check(x.to(dtype).cuda(), numbers(rows, 10), top_k=top_k, temperature=0.8)
+
+
 def test_no_rows():
     out = vsb.sample(torch.empty((0, 64), device="cuda"), torch.empty(0, device="cuda"))
     assert out["token"].numel() == 0

@@ -64,6 +64,18 @@ def test_ties_and_crowds(dtype, k):
 
 
 @pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("k", [1, 256, 1024])
+def test_largest_vocabulary(dtype, k):
+    """Rows that no cluster's shared memory holds, and one in between, one of
+    them a crowd."""
+    for vocab in (1 << 20, 300_001):
+        x = logits_on("cuda", 3, vocab, dtype, seed=k)
+        x[1, :vocab] = 1.0
+        x[1, 1000:vocab:1000] = 2.0
+        check(x, k, vocab)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
 def test_masked_and_bad_rows(dtype):
     rows, vocab, k = 8, 5003, 40
     x = logits_on("cuda", rows, vocab, dtype, seed=2)
