@@ -444,7 +444,8 @@ vs_status vs_support_lmhead_score(int32_t rows, int32_t vocab, int32_t hidden_di
                                   const vs_score_out* out, float* support_logits,
                                   int64_t logits_ld, void* stream);
 
-/* Largest vocabulary of vs_sample, vs_topk_logprob and vs_distill_*. */
+/* Largest vocabulary of vs_sample, vs_topk_logprob and vs_distill_*; they take
+ * up to 2^24 rows (VS_ERR_UNSUPPORTED beyond either). */
 #define VS_MAX_ROW_VOCAB (1 << 20)
 /* Largest k of vs_topk_logprob. */
 #define VS_MAX_TOPK 1024
@@ -498,8 +499,8 @@ vs_status vs_sample(const vs_sample_args* args, int32_t* token, float* logprob,
  * (vs_fused_lmhead_score gives the same two outputs from hidden states).
  * ids and logprob are [rows, out_ld], the first k of each row written; -1 and
  * -inf where the row has fewer than k unmasked (not -inf) tokens.  Rows with a
- * NaN or +inf logit, or a temperature that is not positive and finite: -1 and
- * NaN (status as for vs_sample).  1 <= k <= min(vocab, VS_MAX_TOPK);
+ * NaN or +inf logit, or a temperature that is not finite or below 2^-126 (1 / T
+ * has to be finite): -1 and NaN (status as for vs_sample).  1 <= k <= min(vocab, VS_MAX_TOPK);
  * VS_ERR_UNSUPPORTED beyond VS_MAX_TOPK or VS_MAX_ROW_VOCAB.  logprob and
  * status may be NULL.  No workspace. */
 vs_status vs_topk_logprob(int32_t rows, int32_t vocab, int64_t ld, vs_dtype dtype,
@@ -514,7 +515,7 @@ typedef struct vs_distill_args {
   int64_t ld;    /* row stride of logits, in elements, >= vocab */
   vs_dtype dtype;
   const void* logits;       /* [R, ld] the student's */
-  const float* temperature; /* [R] (> 0, finite), or NULL to use temperature_scalar */
+  const float* temperature; /* [R] (>= 2^-126, finite), or NULL to use temperature_scalar */
   float temperature_scalar;
   /* the teacher's list: [R, teacher_ld], the first teacher_width of each row
    * used; -1 = padding anywhere in the row */

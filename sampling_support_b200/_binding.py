@@ -593,12 +593,14 @@ def _row_logits(logits, vocab):
     if logits.dim() != 2:
         raise ValueError("logits must be [rows, ld]")
     rows, width = logits.shape
+    if rows > 1 << 24:
+        raise ValueError("logits must have at most 2^24 rows")
     ld, unit = logits.stride()
     if unit != 1 and width > 1:
         raise ValueError("logits must have unit stride along the vocabulary")
     vocab = width if vocab is None else int(vocab)
-    if vocab > width:
-        raise ValueError(f"vocab {vocab} exceeds the {width} columns of logits")
+    if not 0 <= vocab <= width:
+        raise ValueError(f"vocab {vocab} is not within the {width} columns of logits")
     if rows <= 1:  # the stride of a single row says nothing: its width, in whole vectors
         per = 16 // logits.element_size()
         ld = (max(width, 1) + per - 1) // per * per
@@ -617,6 +619,12 @@ def _row_setting(v, name, rows, dtype, device):
         _check_tensor(v, name, (rows,), dtype, device)
         return v.data_ptr(), 0
     return None, v
+
+
+def _int32(v):
+    """An integer as the library takes it: beyond the type's range its nearest
+    value (which disables or refuses as the number itself would), never wrapped."""
+    return max(-1 << 31, min(int(v), (1 << 31) - 1))
 
 
 def _tensors(*values):
@@ -638,7 +646,7 @@ def sample(logits, uniform, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0, voca
     p_at, p = _row_setting(top_p, "top_p", rows, torch.float32, dev)
     m_at, m = _row_setting(min_p, "min_p", rows, torch.float32, dev)
     dev = _cuda_device(logits)
-    a = SampleArgs(rows, vocab, ld, _dtype_code(logits), logits.data_ptr(), t_at, float(t), k_at, int(k),
+    a = SampleArgs(rows, vocab, ld, _dtype_code(logits), logits.data_ptr(), t_at, float(t), k_at, _int32(k),
                    p_at, float(p), m_at, float(m), uniform.data_ptr())
     token = torch.empty(rows, dtype=torch.int32, device=dev)
     logprob = torch.empty_like(uniform)
@@ -658,9 +666,10 @@ def topk_logprob(logits, k, temperature=1.0, vocab=None, stream=None):
     rows, vocab, ld = _row_logits(logits, vocab)
     dev = _cuda_device(logits)
     t_at, t = _row_setting(temperature, "temperature", rows, torch.float32, dev)
-    k = int(k)
-    ids = torch.empty((rows, max(k, 0)), dtype=torch.int32, device=dev)
-    logprob = torch.empty((rows, max(k, 0)), dtype=torch.float32, device=dev)
+    k = _int32(k)
+    room = max(0, min(k, VS_MAX_TOPK))  # a k beyond it is refused below
+    ids = torch.empty((rows, room), dtype=torch.int32, device=dev)
+    logprob = torch.empty((rows, room), dtype=torch.float32, device=dev)
     status = torch.empty(rows, dtype=torch.int32, device=dev)
     _launch(load().vs_topk_logprob, (rows, vocab, ld, _dtype_code(logits), logits.data_ptr(), t_at, float(t), k,
                                      ids.data_ptr(), logprob.data_ptr(), k, status.data_ptr()), dev, stream,

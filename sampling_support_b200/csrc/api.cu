@@ -469,7 +469,7 @@ vs_status vs_support_lmhead_score(int32_t rows, int32_t vocab, int32_t hidden_di
 
 namespace {
 
-// vocab * 2^shift <= 2^63
+// vocab * 2^shift <= 2^62
 int row_fx_shift(int32_t vocab) {
   int bits = 0;
   while ((1ll << bits) < static_cast<long long>(vocab)) ++bits;
@@ -502,8 +502,8 @@ vs_status check_distill(const vs_distill_args* a) {
   if (a->teacher_ld < a->teacher_width)
     return fail(VS_ERR_INVALID_ARG, "teacher_ld must be >= teacher_width");
   if (a->tail != 0 && a->tail != 1) return fail(VS_ERR_INVALID_ARG, "tail must be 0 or 1");
-  if (!a->temperature && !(std::isfinite(a->temperature_scalar) && a->temperature_scalar > 0.f))
-    return fail(VS_ERR_INVALID_ARG, "temperature_scalar must be finite and > 0");
+  if (!a->temperature && !(std::isfinite(a->temperature_scalar) && a->temperature_scalar >= vs::kLeastT))
+    return fail(VS_ERR_INVALID_ARG, "temperature_scalar must be finite and >= 2^-126");
   if (a->rows > 0 && a->teacher_width > 0 && (!a->teacher_ids || !a->teacher_logprob))
     return fail(VS_ERR_INVALID_ARG, "teacher_ids and teacher_logprob must be non-NULL");
   return VS_OK;
@@ -591,8 +591,8 @@ vs_status vs_topk_logprob(int32_t rows, int32_t vocab, int64_t ld, vs_dtype dtyp
                           uint32_t* status, void* stream) {
   const vs_status st = check_rows(rows, vocab, ld, dtype, logits);
   if (st != VS_OK) return st;
-  if (!temperature && !(std::isfinite(temperature_scalar) && temperature_scalar > 0.f))
-    return fail(VS_ERR_INVALID_ARG, "temperature_scalar must be finite and > 0");
+  if (!temperature && !(std::isfinite(temperature_scalar) && temperature_scalar >= vs::kLeastT))
+    return fail(VS_ERR_INVALID_ARG, "temperature_scalar must be finite and >= 2^-126");
   if (k < 1 || k > vocab) return fail(VS_ERR_INVALID_ARG, "k must lie in [1, vocab]");
   if (k > VS_MAX_TOPK) return fail(VS_ERR_UNSUPPORTED, "k exceeds VS_MAX_TOPK");
   if (out_ld < k) return fail(VS_ERR_INVALID_ARG, "out_ld must be >= k");

@@ -209,7 +209,7 @@ __global__ void __launch_bounds__(kDThreads) distill_fwd_kernel(DistillParams P)
   const Raw* x = static_cast<const Raw*>(P.logits) + static_cast<int64_t>(row) * P.ld;
   const int j0 = min(V, rank * P.chunk), j1 = min(V, j0 + P.chunk);
   const float t = P.temperature ? P.temperature[row] : P.temperature_scalar;
-  const bool fine = t > 0.f && t < kInf;
+  const bool fine = t >= kLeastT && t < kInf;
   const float c = fminf(kLog2e / t, 3e38f);
 
   // the list: marks over the whole vocabulary, repeats found on the way
@@ -459,7 +459,7 @@ __global__ void __launch_bounds__(kSThreads, 5) distill_stage_kernel(DistillPara
   __syncwarp();
   asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");  // ordered by the fence above
   const float t = P.temperature ? P.temperature[row] : P.temperature_scalar;
-  const bool fine = t > 0.f && t < kInf;
+  const bool fine = t >= kLeastT && t < kInf;
   const float c = fminf(kLog2e / t, 3e38f);
   const bool tail = P.tail != 0;
   for (int i = n / 8 * 8 + tid; i < groups * 8; i += kSThreads) buf[i] = i < n ? x[j0 + i] : kMasked;

@@ -114,6 +114,10 @@ struct SampleParams {
   int32_t lists;     // the list kernel takes the rows with a small top-k
 };
 
+// Smallest temperature of the log-probabilities and of the distillation: below it 1 / T leaves
+// fp32's range.
+constexpr float kLeastT = 1.17549435e-38f;  // 2^-126
+
 // Largest top-k of vs_sample that is taken from a list of the row's largest
 // elements.  A greedy row is one of them.
 constexpr int kListTopK = 512;

@@ -639,7 +639,7 @@ __device__ __forceinline__ void topk_row(const TopkParams& P, int row) {
   float* lps = P.logprob ? P.logprob + static_cast<int64_t>(row) * P.out_ld : nullptr;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const float t = P.temperature ? P.temperature[row] : P.temperature_scalar;
-  const bool fine = t > 0.f && t < kInf;
+  const bool fine = t >= kLeastT && t < kInf;
 
   cta_sync();  // the geometry
   const uint32_t kmax = rs_max<Raw>();

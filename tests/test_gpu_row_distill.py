@@ -254,6 +254,20 @@ def test_rows_without_a_loss(tail):
     assert (grad[:, :vocab] == 0).all() and (out["grad"][:, :vocab] == 0).all()
 
 
+def test_smallest_temperatures():
+    vocab = 901
+    x = logits_on("cuda", 2, vocab, F32, seed=13)
+    x[1, :vocab] = 3.0  # every difference is zero, whatever T
+    ids, lp = torch.full((2, 1), 7, dtype=torch.int32).cuda(), torch.full((2, 1), -1.0).cuda()
+    kw = dict(temperature=torch.tensor([2.0 ** -127, 2.0 ** -126]).cuda(), tail=True, vocab=vocab)
+    out = vsb.distill_fwd(x, ids, lp, want_grad=True, grad_dtype=F32, **kw)
+    grad = vsb.distill_bwd(x, ids, lp, out["ctx"], **kw)
+    torch.cuda.synchronize()
+    assert out["status"].tolist() == [vsb.ROW_BAD_PARAM, 0] and (grad[0, :vocab] == 0).all()
+    assert torch.isnan(out["loss"][0]) and torch.isfinite(out["loss"][1])
+    assert torch.isfinite(grad[:, :vocab]).all() and torch.isfinite(out["grad"][:, :vocab]).all()
+
+
 def test_gradient_by_differences():
     """The gradient predicts how the kernel's own loss moves: along a direction
     d of unit steps of 2^-6, the central difference of the fp32 losses is off by

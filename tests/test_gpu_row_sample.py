@@ -104,7 +104,7 @@ def test_equal_logits_cut_exactly(dtype, vocab):
 
 
 @pytest.mark.parametrize("dtype", [BF, F32])
-@pytest.mark.parametrize("temperature", [1e-30, 1e-3, 0.05, 30.0, 1e6])
+@pytest.mark.parametrize("temperature", [1e-40, 1e-30, 1e-3, 0.05, 30.0, 1e6])
 def test_temperatures(dtype, temperature):
     x = logits_on("cuda", 8, 12_000, dtype, seed=4)
     for kw in (dict(), dict(top_p=0.7), dict(top_k=20), dict(top_k=3000), dict(min_p=0.3)):
@@ -220,6 +220,55 @@ def test_another_stream_and_a_captured_call():
         torch.cuda.synchronize()
         for g, out, kw in graphs:
             compare(out, x, u, 30_000, **kw)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("vocab", [515, 40_000])
+def test_zeros_of_either_sign_are_equal(dtype, vocab):
+    x = logits_on("cuda", 6, vocab, dtype, seed=15)
+    x[x.abs() < 0.7] = 0.0
+    x[:, ::3] *= -1.0  # zeros of both signs, in no order
+    x[2:] = x[2:].clamp(max=0.0)  # and as the largest values
+    x[4:, 5::7] = 2.0 ** -40  # next to values near them
+    u = numbers(6, 9)
+    for kw in (dict(top_k=3), dict(top_k=vocab // 5), dict(top_p=0.3), dict(min_p=0.9), dict(temperature=0.0), {}):
+        check(x, u, vocab, **kw)
+
+
+def test_calls_at_once_from_two_threads():
+    import threading
+
+    x = [logits_on("cuda", rows, 60_000, dtype, seed=16) for rows, dtype in ((3, BF), (20, F32))]
+    u = [numbers(3, 10), numbers(20, 11)]
+    kw = [dict(top_p=0.9), dict(top_k=30)]
+    torch.cuda.synchronize()
+    outs = [[], []]
+
+    def work(i):
+        stream = torch.cuda.Stream()
+        for _ in range(40):
+            outs[i].append(vsb.sample(x[i], u[i], stream=stream, **kw[i]))
+            outs[i].append(vsb.topk_logprob(x[i], 50, stream=stream))
+        stream.synchronize()
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    for i in range(2):
+        compare(outs[i][0], x[i], u[i], 60_000, **kw[i])
+        for j, out in enumerate(outs[i]):
+            for name, t in out.items():
+                assert torch.equal(t, outs[i][j % 2][name]), (i, j, name)
+
+
+def test_a_top_k_beyond_32_bits_keeps_every_token():
+    x, u = logits_on("cuda", 2, 1000, F32, seed=17), numbers(2, 12)
+    out = vsb.sample(x, u, top_k=(1 << 32) + 1, vocab=1000)
+    assert out["support_size"].tolist() == [1000, 1000]
+    with pytest.raises(vsb.VsError):
+        vsb.topk_logprob(x, (1 << 32) + 1)
 
 
 def test_offsets_beyond_32_bits():

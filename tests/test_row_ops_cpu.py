@@ -52,6 +52,8 @@ def test_topk_refuses():
                dict(logits=FAKE + 4), dict(temp=0.0), dict(temp=float("nan")), dict(k=0), dict(k=1001, out_ld=1001),
                dict(out_ld=7), dict(ids=0)):
         assert _topk(**kw) == INV, kw
+    assert _topk(temp=2.0 ** -127) == INV  # 1 / T is not finite in fp32
+    assert _topk(rows=(1 << 24) + 1) == UNS
     assert _topk(vocab=4000, ld=4000, k=1025, out_ld=1025) == UNS
     assert _topk(vocab=B.VS_MAX_ROW_VOCAB + 4, ld=B.VS_MAX_ROW_VOCAB + 4) == UNS
     assert _topk(rows=0, logits=0, ids=0) == B.VS_OK
@@ -68,7 +70,8 @@ def _distill_args(**kw):
 BAD_DISTILL = [
     (dict(rows=-1), INV), (dict(vocab=0), INV), (dict(ld=999), INV), (dict(ld=1004), INV), (dict(dtype=5), INV),
     (dict(logits=0), INV), (dict(logits=FAKE + 8), INV), (dict(temperature_scalar=0.0), INV),
-    (dict(temperature_scalar=float("inf")), INV), (dict(teacher_ids=0), INV), (dict(teacher_logprob=0), INV),
+    (dict(temperature_scalar=float("inf")), INV), (dict(temperature_scalar=2.0 ** -127), INV),
+    (dict(rows=(1 << 24) + 1), UNS), (dict(teacher_ids=0), INV), (dict(teacher_logprob=0), INV),
     (dict(teacher_ld=7), INV), (dict(tail=2), INV), (dict(teacher_width=-1), UNS),
     (dict(teacher_width=1025, teacher_ld=1025), UNS),
     (dict(vocab=B.VS_MAX_ROW_VOCAB + 8, ld=B.VS_MAX_ROW_VOCAB + 8), UNS),
@@ -126,6 +129,11 @@ def test_binding_refuses_host_tensors_and_wrong_shapes():
         vsb.sample(x, torch.zeros(2), vocab=17)
     with pytest.raises(ValueError):
         vsb.sample(x.t(), torch.zeros(16))
+    with pytest.raises(ValueError):
+        vsb.sample(x, torch.zeros(2), vocab=-(1 << 32) + 16)
+    with pytest.raises(ValueError):
+        vsb.sample(torch.zeros(1, 8).expand((1 << 24) + 1, 8), torch.zeros(1).expand((1 << 24) + 1))
+    assert [B._int32(v) for v in (7, (1 << 32) + 1, -(1 << 40))] == [7, (1 << 31) - 1, -(1 << 31)]
     with pytest.raises(ValueError):
         vsb.topk_logprob(x, 4)
     with pytest.raises(TypeError):
