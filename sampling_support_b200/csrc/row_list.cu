@@ -4,7 +4,7 @@
 // A cluster stages the row in its CTAs' shared memory (one bulk copy per
 // slice, so the row is read from HBM once) and finds a floor that at least k
 // elements reach: every thread's two largest group maxima are elements of their own,
-// so a value that k of any CTA's maxima reach is a floor, and so is the smallest
+// (all elements of a slice that is short) so a value that k of any CTA's maxima reach is a floor, and so is the smallest
 // over the CTAs of values that ceil(k / C) of theirs reach.  The elements from the floor
 // up (hardly more than k) are listed, gathered by the leader and sorted there.
 // Top-k adds the row's sum of exponentials, taken in the same pass as the
@@ -17,6 +17,8 @@
 // leaves once they are sent unless it has listed more.  Where the list
 // overflows (crowds of equal values) the leader alone selects by digits of the
 // key from the row in L2: some passes of one CTA, for rows that are rare.
+#include <stddef.h>
+
 #include <algorithm>
 
 #include "internal.h"
@@ -32,8 +34,10 @@ constexpr int kLWarps = kLThreads / 32;
 constexpr int kLMaxCluster = 8;
 constexpr int kLTotal = 4096;  // listed elements per row, at most
 constexpr int kLBins = 512;    // of the vector maxima, linear in the value below the largest
-// Listed elements per CTA: 256 keep five CTAs on an SM, wide lists take 1,024.
-__host__ __device__ inline int list_local(int k) { return k <= 256 ? 256 : 1024; }
+constexpr int kLShort = 4096;  // a slice of at most so many elements can bin them all
+// Listed elements per CTA: 256 keep five CTAs on an SM, wide lists take 1,024
+// (a CTA that lists alone holds k and what shares its floor's bin).
+__host__ __device__ inline int list_local(int k, int c) { return k <= (c > 1 ? 256 : 192) ? 256 : 1024; }
 
 struct alignas(16) ListPart {
   uint32_t kmax;         // largest key
@@ -102,10 +106,90 @@ __device__ __forceinline__ int bin_reaching(uint32_t upto, uint32_t mine, const 
   return __shfl_sync(0xffffffffu, b, l) + l * (kLBins / 32);
 }
 
+// Brings a list of n > 1,024 elements down to its largest, at least `keep` and
+// at most 1,024 of them, in place: the smallest of those from counts over the
+// words' range, 1,024 bins at a time, zooming into the bin that `keep` falls
+// in as long as it holds too many (the words differ, so one of them does not).
+// Returns how many stay.  Long lists come from vocabularies of a few thousand
+// tokens with a k of that order, where the maxima give no floor: sorting 4,096
+// elements there took most of 127 us (58 x 2,876 bf16, k 727).
+__device__ __noinline__ uint32_t list_shrink(u64* list, uint32_t n, uint32_t keep, ListStage& sh) {
+  constexpr int kBins = 2 * kLBins, kMost = 4 * kLThreads;
+  static_assert(kBins == 1024 && offsetof(ListStage, least) == offsetof(ListStage, bins) + sizeof(sh.bins), "one array");
+  uint32_t* bins = sh.bins;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  uint32_t kmax = 0u, kmin = 0xFFFFFFFFu;
+  for (uint32_t i = tid; i < n; i += kLThreads) {
+    const uint32_t k = static_cast<uint32_t>(list[i] >> 32);
+    kmax = max(kmax, k);
+    kmin = min(kmin, k);
+  }
+  kmax = __reduce_max_sync(0xffffffffu, kmax);
+  kmin = __reduce_min_sync(0xffffffffu, kmin);
+  cta_sync();
+  if (lane == 0) {
+    sh.rmax[warp] = kmax;
+    sh.rmin[warp] = kmin;
+  }
+  cta_sync();
+  kmax = __reduce_max_sync(0xffffffffu, lane < kLWarps ? sh.rmax[lane] : 0u);
+  kmin = __reduce_min_sync(0xffffffffu, lane < kLWarps ? sh.rmin[lane] : 0xFFFFFFFFu);
+  u64 hi = static_cast<u64>(kmax) << 32 | 0xFFFFFFFFull, lo = static_cast<u64>(kmin) << 32;
+  uint32_t before = 0u;  // elements above hi
+  for (;;) {
+    const int shift = max(0, 64 - __clzll(hi - lo) - 10);
+    cta_sync();
+    for (int i = tid; i < kBins; i += kLThreads) bins[i] = 0u;
+    cta_sync();
+    for (uint32_t i = tid; i < n; i += kLThreads) {
+      const u64 w = list[i];
+      if (w >= lo && w <= hi) atomicAdd(&bins[(hi - w) >> shift], 1u);
+    }
+    cta_sync();
+    // every warp: first the 32 bins, then the one of them, in which the count reaches `keep`
+    uint32_t sum = 0u;
+#pragma unroll 8
+    for (int i = 0; i < 32; ++i) sum += bins[lane * 32 + (i ^ lane)];
+    uint32_t upto = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint32_t a = __shfl_up_sync(0xffffffffu, upto, o);
+      if (lane >= o) upto += a;
+    }
+    const int l = __ffs(__ballot_sync(0xffffffffu, before + upto >= keep) | 0x80000000u) - 1;
+    before += __shfl_sync(0xffffffffu, upto - sum, l);
+    const uint32_t c = bins[l * 32 + lane];
+    uint32_t run = c;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint32_t a = __shfl_up_sync(0xffffffffu, run, o);
+      if (lane >= o) run += a;
+    }
+    const int b = __ffs(__ballot_sync(0xffffffffu, before + run >= keep) | 0x80000000u) - 1;
+    const uint32_t through = before + __shfl_sync(0xffffffffu, run, b);
+    before += __shfl_sync(0xffffffffu, run - c, b);
+    hi -= static_cast<u64>(l * 32 + b) << shift;
+    const u64 width = (1ull << shift) - 1ull;
+    lo = hi - lo > width ? hi - width : lo;
+    if (through <= static_cast<uint32_t>(kMost) || shift == 0) break;
+  }
+  // the elements from lo up, to the front: a round of them is read before its places are written
+  if (tid == 0) sh.bad = 0u;
+  for (uint32_t i0 = 0; i0 < n; i0 += kLThreads) {
+    const u64 w = i0 + tid < n ? list[i0 + tid] : 0ull;
+    cta_sync();
+    const bool in = i0 + tid < n && w >= lo;
+    const uint32_t at = in ? atomicAdd(&sh.bad, 1u) : 0u;
+    if (in && at < static_cast<uint32_t>(kMost)) list[at] = w;
+  }
+  cta_sync();
+  return min(sh.bad, static_cast<uint32_t>(kMost));
+}
+
 // The n listed elements in descending order at `out` (the first `keep`; room
 // for kListTopK) or, for more than a block's worth, sorted in place.  Returns
 // where they are.
-__device__ __forceinline__ u64* list_sort(u64* list, u64* out, uint32_t n, uint32_t keep) {
+__device__ __forceinline__ u64* list_sort(u64* list, u64* out, uint32_t n, uint32_t keep, ListStage& sh) {
   if (n <= kLThreads) {
     int bits = 3;
     while ((1u << bits) < n) ++bits;
@@ -119,25 +203,15 @@ __device__ __forceinline__ u64* list_sort(u64* list, u64* out, uint32_t n, uint3
     cta_sync();
     return out;
   }
-  uint32_t m = 2 * kLThreads;
-  while (m < n) m *= 2;
-  for (uint32_t i = n + threadIdx.x; i < m; i += kLThreads) list[i] = 0ull;
-  for (uint32_t size = 2; size <= m; size <<= 1)
-    for (uint32_t step = size >> 1; step > 0; step >>= 1) {
-      cta_sync();
-      for (uint32_t i = threadIdx.x; i < m / 2; i += kLThreads) {
-        const uint32_t a = 2 * i - (i & (step - 1)), b = a + step;
-        const u64 x = list[a], y = list[b];
-        if (((a & size) == 0u) == (x < y)) {
-          list[a] = y;
-          list[b] = x;
-        }
-      }
-    }
-  cta_sync();
+  if (n > 4 * kLThreads) n = list_shrink(list, n, keep, sh);
+  if (n <= 2 * kLThreads)
+    block_sort<kLThreads, 2>(list, list, n);
+  else
+    block_sort<kLThreads, 4>(list, list, n);
   return list;
 }
-static_assert(kLThreads <= kListTopK && (kLTotal & (kLTotal - 1)) == 0, "the sorted copy's room, and the padded list's");
+static_assert(kLThreads <= kListTopK && 4 * kLThreads >= VS_MAX_TOPK && 4 * kLThreads >= kListTopK,
+              "the sorted copy's room, and what is sorted in place");
 
 // vs_topk_logprob: rows[k] ids and log-probabilities.
 struct TopkOp {
@@ -150,7 +224,7 @@ struct TopkOp {
   }
   __device__ __forceinline__ static bool fine(const Params& P, int row) {
     const float t = t_of(P, row);
-    return t > 0.f && t < kInf;
+    return t >= kLeastT && t < kInf;
   }
   // no list: bad input, or every token masked
   __device__ __forceinline__ static void none(const Params& P, int row, uint32_t status) {
@@ -455,11 +529,28 @@ __global__ void __launch_bounds__(kLThreads, 5) list_kernel(const __grid_constan
     top[1] = ListKey<Raw>::of(two.second);
     mine = two.first != two.first ? 0xFFFFFFFFu : top[0];
   }
+  // a short slice gives all its elements to the bins when its maxima are too few for a near floor: a
+  // share of a third of the groups still leaves a list of 1.2 times its length (bins for every
+  // element cost 948 rows of 2,785 about 4 us)
+  const bool every = groups * 8 <= kLShort && 3 * ((k + C - 1) / C) >= groups;
+  auto candidates = [&](auto&& f) {
+    if (!every) {
+      f(top[0]);
+      f(top[1]);
+    } else {
+      for (int g = tid; g < groups; g += kLThreads) {
+        Eight<Raw> v;
+        v.load(buf + g * 8);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) f(key_of(v.e[i]));
+      }
+    }
+  };
   {
     uint32_t low = 0xFFFFFFFFu;
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-      if (top[i] > ListKey<Raw>::kMasked) low = min(low, top[i]);
+    candidates([&](uint32_t key) {
+      if (key > ListKey<Raw>::kMasked) low = min(low, key);
+    });
     const uint32_t wmax = __reduce_max_sync(0xffffffffu, mine), wmin = __reduce_min_sync(0xffffffffu, low);
     if (lane == 0) {
       sh.rmax[warp] = wmax;
@@ -473,13 +564,13 @@ __global__ void __launch_bounds__(kLThreads, 5) list_kernel(const __grid_constan
     // bins over the maxima's range, at most 100 below the largest (masks by a huge negative value)
     const float high = KeyTraits<Raw>::decode(bmax), range = fminf(high - KeyTraits<Raw>::decode(bmin), 100.f);
     const float per = range > 0.f ? fminf((kLBins - 1) / range, 1e30f) : 0.f;
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-      if (top[i] > ListKey<Raw>::kMasked) {
-        const int b = static_cast<int>(fminf((high - KeyTraits<Raw>::decode(top[i])) * per, kLBins - 1.f));
+    candidates([&](uint32_t key) {
+      if (key > ListKey<Raw>::kMasked) {
+        const int b = static_cast<int>(fminf((high - KeyTraits<Raw>::decode(key)) * per, kLBins - 1.f));
         atomicAdd(&sh.bins[b], 1u);
-        atomicMin(&sh.least[b], top[i]);
+        atomicMin(&sh.least[b], key);
       }
+    });
   }
   cta_sync();
   asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
@@ -594,7 +685,7 @@ __global__ void __launch_bounds__(kLThreads, 5) list_kernel(const __grid_constan
   }
   const uint32_t nk = min(static_cast<uint32_t>(k), total);
   u64* spare = list + list_total(C, local);
-  u64* sorted = list_sort(list, spare, total, nk);
+  u64* sorted = list_sort(list, spare, total, nk, sh);
   float z = 0.f;
   if constexpr (Op::kSum)
     z = warp_sum(lane < C && p.z != 0.f ? p.z * ex2((p.m - vmax) * c) : 0.f);
@@ -605,11 +696,13 @@ template <typename Raw, typename Op>
 cudaError_t launch_list(const typename Op::Params& P, cudaStream_t s, bool* done) {
   int c = stage_cluster_size(P.rows, P.vocab, sizeof(Raw));
   *done = c != 0;
-  // wide lists: a CTA's share of k stays well below its 512 maxima and its list
-  while (c != 0 && c < kLMaxCluster && Op::most(P) > 128 * c) c *= 2;
+  // wide lists: a CTA's share of k stays well below its 512 maxima (unless it bins all its elements:
+  // 948 x 2,785 bf16, k 161: 26.7 us with one CTA per row, 39 with two) and below its list
+  const int most = Op::most(P);
+  while (c != 0 && c < kLMaxCluster && ((most > 128 * c && P.vocab > kLShort * c) || most > 768 * c)) c *= 2;
   if (c == 0) return cudaSuccess;
   const int chunk = ((P.vocab + c - 1) / c + 31) / 32 * 32;
-  const int local = list_local(std::max(Op::most(P), 1));
+  const int local = list_local(std::max(most, 1), c);
   const size_t smem = sizeof(ListStage) + list_room(c, local, static_cast<size_t>(chunk) * sizeof(Raw));
   return launch_cluster<list_kernel<Raw, Op>>(static_cast<unsigned>(P.rows) * c, c, kLThreads, smem, false, s, P, chunk,
                                               local);

@@ -538,8 +538,7 @@ static_assert(kRsWarps % kRsMaxCluster == 0, "every peer's list has its warps");
 // Leader: the first `keep` of the n collected elements in the total order
 // (descending words: value, then smaller id), into sh.sorted.  Up to 512
 // elements: an element's place is the number of larger ones, counted by a
-// group of 512 / 2^ceil(log2 n) neighbouring lanes; more: a bitonic network
-// (its 66 to 78 steps against the count's n / 2 double loads).
+// group of 512 / 2^ceil(log2 n) neighbouring lanes; more: a bitonic network.
 static __device__ __noinline__ void rs_sort(uint32_t n, uint32_t keep) {
   RsShared& sh = rs_shared();
   int bits = kRsLog - 5;
@@ -557,23 +556,14 @@ static __device__ __noinline__ void rs_sort(uint32_t n, uint32_t keep) {
     cta_sync();
     return;
   }
-  const uint32_t m = 1u << bits;
-  for (uint32_t i = threadIdx.x; i < m; i += kRsThreads) sh.sorted[i] = i < n ? sh.list[i] : 0ull;
-  for (uint32_t size = 2; size <= m; size <<= 1)
-    for (uint32_t step = size >> 1; step > 0; step >>= 1) {
-      cta_sync();
-      for (uint32_t i = threadIdx.x; i < m / 2; i += kRsThreads) {
-        const uint32_t a = 2 * i - (i & (step - 1)), b = a + step;
-        const u64 x = sh.sorted[a], y = sh.sorted[b];
-        if (((a & size) == 0u) == (x < y)) {
-          sh.sorted[a] = y;
-          sh.sorted[b] = x;
-        }
-      }
-    }
-  cta_sync();
+  if (n <= 2 * kRsThreads)
+    block_sort<kRsThreads, 2>(sh.list, sh.sorted, n);
+  else if (n <= 4 * kRsThreads)
+    block_sort<kRsThreads, 4>(sh.list, sh.sorted, n);
+  else
+    block_sort<kRsThreads, 8>(sh.list, sh.sorted, n);
 }
-static_assert((kRsCap & (kRsCap - 1)) == 0, "rs_sort: the padding stays within the list's room");
+static_assert(kRsCap == 8 * kRsThreads, "block_sort's room");
 
 // Leader: the masses of the first n sorted elements, in sh.list.
 template <typename Raw>

@@ -12,6 +12,8 @@
 
 namespace vs {
 
+using u64 = unsigned long long;
+
 // Eight elements of a row from j (a multiple of 8; j + 8 <= the row's end).
 template <typename T>
 union Eight {
@@ -87,6 +89,67 @@ struct TwoMax {
     first = max_nan(first, t);
   }
 };
+
+// Block of T threads: n <= T E words from src in descending order to dst (room
+// for T E; may be src), zeros behind them.  A bitonic network over E
+// neighbouring words per thread: most of its steps stay in registers or go
+// through the warp's shuffles, log2(T / 32) (log2(T / 32) + 1) / 2 of them
+// through dst (a network through shared memory alone took 1.3 us a step for
+// 4,096 words and 256 threads).
+template <int T, int E>
+__device__ __forceinline__ void block_sort(const u64* src, u64* dst, uint32_t n) {
+  const uint32_t base = threadIdx.x * E;
+  u64 e[E];
+#pragma unroll
+  for (int r = 0; r < E; ++r) e[r] = base + r < n ? src[base + r] : 0ull;
+  auto order = [](u64& a, u64& b, bool descending) {
+    const u64 x = a, y = b;
+    const bool swap = (x < y) == descending;
+    a = swap ? y : x;
+    b = swap ? x : y;
+  };
+#pragma unroll
+  for (int size = 2; size < E; size <<= 1)
+#pragma unroll
+    for (int step = size >> 1; step > 0; step >>= 1)
+#pragma unroll
+      for (int r = 0; r < E; ++r)
+        if (!(r & step)) order(e[r], e[r + step], !(r & size));
+#pragma unroll 1
+  for (uint32_t size = E; size <= T * E; size <<= 1) {
+    const bool descending = (base & size) == 0u;
+#pragma unroll 1
+    for (uint32_t step = size >> 1; step >= E; step >>= 1) {
+      const bool larger = descending == ((base & step) == 0u);
+      if (step < 32u * E) {
+#pragma unroll
+        for (int r = 0; r < E; ++r) {
+          const u64 o = __shfl_xor_sync(0xffffffffu, e[r], step / E);
+          e[r] = (e[r] < o) == larger ? o : e[r];
+        }
+      } else {
+        cta_sync();
+#pragma unroll
+        for (int r = 0; r < E; ++r) dst[base + r] = e[r];
+        cta_sync();
+#pragma unroll
+        for (int r = 0; r < E; ++r) {
+          const u64 o = dst[(base ^ step) + r];
+          e[r] = (e[r] < o) == larger ? o : e[r];
+        }
+      }
+    }
+#pragma unroll
+    for (int step = E >> 1; step > 0; step >>= 1)
+#pragma unroll
+      for (int r = 0; r < E; ++r)
+        if (!(r & step)) order(e[r], e[r + step], descending);
+  }
+  cta_sync();
+#pragma unroll
+  for (int r = 0; r < E; ++r) dst[base + r] = e[r];
+  cta_sync();
+}
 
 // N 16-byte words into a peer's shared memory, counted on its barrier there.
 template <int N>

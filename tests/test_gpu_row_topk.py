@@ -45,6 +45,17 @@ def test_sizes(dtype, vocab, k, rows):
 
 
 @pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("vocab,k,rows", [(2876, 727, 58), (2785, 161, 300), (4096, 192, 200), (4099, 193, 40),
+                                          (4096, 768, 30), (4096, 769, 30), (8001, 1024, 20), (1100, 1024, 9)])
+def test_wide_lists_of_small_vocabularies(dtype, vocab, k, rows):
+    x = logits_on("cuda", rows, vocab, dtype, seed=vocab + k)
+    x[0, : vocab // 2] = float("-inf")
+    x[1, k // 2 : vocab] = float("-inf")  # fewer than k tokens
+    x[2, : vocab - 5] = torch.randint(0, 3, (vocab - 5,), generator=torch.Generator().manual_seed(k)).to(dtype).cuda()
+    check(x, k, vocab, temperature=1.1)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
 @pytest.mark.parametrize("k", [1, 20, 700])
 def test_ties_and_crowds(dtype, k):
     """Equal values beyond any list's room, sorted rows, few distinct values,
