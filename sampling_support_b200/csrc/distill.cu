@@ -389,20 +389,47 @@ constexpr int kSWarps = kSThreads / 32;
 constexpr int kSSlice = kSThreads - 32;  // threads of the slice passes
 constexpr int kSMaxCluster = 8;
 
-// One CTA's part of the row's sums of 2^((l - m) c): 48 bytes.
+// One CTA's part of the row's sums of 2^((l - m) c): 48 bytes.  The loss is a
+// difference of logarithms that may be near zero, so what is joined is in fp64
+// from each thread's sum on, and so are the listed elements, which hold most
+// of the mass: with fp32 there the loss was off by up to 1e-7, now by 1e-8.
 struct alignas(16) DistillPart {
-  float mr, zr;  // outside the list: largest logit, and the sum below it
-  float ml, zl;  // its listed elements
+  float mr, ml;   // largest logit outside the list, and of its listed elements
+  double zr, zl;  // the sums below them
   double w, wu;  // sums of the teacher's weight, and of it times (l - ml) c, over its listed elements
-  uint32_t bad, pad[3];
+  uint32_t bad, pad;
 };
+static_assert(sizeof(DistillPart) == 48, "three 16-byte words");
+
+// 2^x for x <= 0 to 3e-10 of itself (0 below 2^-1000): the Taylor polynomial of
+// degree 8 in the fraction, in pairs, a shorter chain than exp2()'s; the list's
+// warp is as long as the slice's passes.
+__device__ __forceinline__ double exp2_below(double x) {
+  const double r = x + 6755399441055744.0;  // 1.5 * 2^52: the integer lands in the low word
+  const double f = (x - (r - 6755399441055744.0)) * 0.69314718055994531, f2 = f * f;
+  const double lo = fma(f2, fma(f, 1.0 / 6.0, 0.5), 1.0 + f);
+  const double hi = fma(f2, fma(f2, 1.0 / 40320.0, fma(f, 1.0 / 5040.0, 1.0 / 720.0)), fma(f, 1.0 / 120.0, 1.0 / 24.0));
+  const double p = fma(f2 * f2, hi, lo);
+  return x >= -1000.0 ? __hiloint2double(__double2hiint(p) + (__double2loint(r) << 20), __double2loint(p)) : 0.0;
+}
+
+// 2^(d c - rest) for a part's distance d <= 0 from the largest: the product's
+// rounding is put back (at d = -20 it would be worth 1e-6), what is left is the
+// exponential's 2^-22, and nothing at d = 0, where most of the mass is.
+__device__ __forceinline__ double part_scale(float d, float c, float rest) {
+  const float p = __fmul_rn(d, c);
+  const float lo = fmaf(d, c, -p) - rest;
+  const float e = ex2(p);
+  return e > 0.f ? static_cast<double>(e) * (1.0 + 0.69314718055994531 * static_cast<double>(lo)) : 0.0;
+}
 
 struct alignas(16) DistillStage {
   DistillPart parts[kSMaxCluster];  // from the CTA of each rank
   DistillCtx k;
   uint64_t bar, xbar;  // the slice's copy; the parts
   double s0, t1, tnorm, at;
-  float2 red[kSWarps];
+  float red_m[kSWarps];
+  double red_z[kSWarps];
   uint32_t status, dup, any, bad;
 };
 
@@ -517,7 +544,8 @@ __global__ void __launch_bounds__(kSThreads, 5) distill_stage_kernel(DistillPara
   }
   cta_sync();
 
-  DistillPart mine{-kInf, 0.f, -kInf, 0.f, 0.0, 0.0, 0u, {0u, 0u, 0u}};
+  DistillPart mine{-kInf, -kInf, 0.0, 0.0, 0.0, 0.0, 0u, 0u};
+  const double cd = static_cast<double>(c);  // the same factor everywhere: its rounding cancels
   if (tid < 32) {
     // the list: the teacher's sums s0 = sum w, t1 = sum w lp with w = exp(lp - off) over all of it, and the
     // student's over this slice's elements
@@ -533,7 +561,8 @@ __global__ void __launch_bounds__(kSThreads, 5) distill_stage_kernel(DistillPara
     lmax = warp_max_nan(lmax);
     double s0 = 0.0, t1 = 0.0, ws = 0.0, wu = 0.0;
     uint32_t bad = lmax < kInf ? 0u : 1u;  // NaN or +inf
-    float zl = 0.f;
+    double zl = 0.0;
+#pragma unroll 1
     for (int s = lane; s < W; s += 32) {
       const int id = ids[s];
       if (id < 0) continue;
@@ -546,10 +575,10 @@ __global__ void __launch_bounds__(kSThreads, 5) distill_stage_kernel(DistillPara
         t1 += w * static_cast<double>(l);
         if (own && w > 0.0) {
           ws += w;
-          if (lmax > -kInf) wu += w * ((static_cast<double>(u) - static_cast<double>(lmax)) * static_cast<double>(c));
+          if (lmax > -kInf) wu += w * ((static_cast<double>(u) - static_cast<double>(lmax)) * cd);
         }
       }
-      if (own && lmax > -kInf) zl += ex2((u - lmax) * c);
+      if (own && lmax > -kInf) zl += exp2_below((static_cast<double>(u) - static_cast<double>(lmax)) * cd);
     }
     mine.ml = lmax;
     mine.zl = warp_sum(zl);
@@ -565,18 +594,23 @@ __global__ void __launch_bounds__(kSThreads, 5) distill_stage_kernel(DistillPara
       sh.at = tail ? fmax(0.0, 1.0 - s0) : 0.0;
     }
   } else {
-    float m, z;
-    slice_sum(buf, tid - 32, groups, kSSlice, c, m, z);
+    float m, z, rest;
+    slice_sum(buf, tid - 32, groups, kSSlice, c, m, z, rest);
     const float wm = warp_max_nan(m);  // a NaN or +inf marks the part
-    z = warp_sum(z != 0.f ? z * ex2((m - wm) * c) : 0.f);
-    if (lane == 0) sh.red[tid >> 5] = make_float2(wm, z);
+    const double zw = warp_sum(z != 0.f ? z * part_scale(m - wm, c, rest) : 0.0);
+    if (lane == 0) {
+      sh.red_m[tid >> 5] = wm;
+      sh.red_z[tid >> 5] = zw;
+    }
   }
   cta_sync();
   asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
   if (tid < 32) {
-    float2 r = lane > 0 && lane < kSWarps ? sh.red[lane] : make_float2(-kInf, 0.f);
-    mine.mr = warp_max_nan(r.x);
-    mine.zr = warp_sum(r.y != 0.f ? r.y * ex2((r.x - mine.mr) * c) : 0.f);
+    const bool in = lane > 0 && lane < kSWarps;
+    const float m = in ? sh.red_m[lane] : -kInf;
+    const double z = in ? sh.red_z[lane] : 0.0;
+    mine.mr = warp_max_nan(m);
+    mine.zr = warp_sum(z != 0.0 ? z * part_scale(m - mine.mr, c, 0.f) : 0.0);
     mine.bad |= sh.bad | (mine.mr < kInf ? 0u : 1u);
     if (lane < (GRAD ? C : 1)) push_words<sizeof(DistillPart) / 16>(peer_addr(&sh.parts[rank], lane), peer_addr(&sh.xbar, lane), &mine);
   }
@@ -586,14 +620,13 @@ __global__ void __launch_bounds__(kSThreads, 5) distill_stage_kernel(DistillPara
   if (tid < 32) {
     const bool got = mbar_wait(&sh.xbar, 0);
     __syncwarp();
-    const DistillPart p = lane < C && got ? sh.parts[lane] : DistillPart{-kInf, 0.f, -kInf, 0.f, 0.0, 0.0, 0u, {0u, 0u, 0u}};
+    const DistillPart p = lane < C && got ? sh.parts[lane] : DistillPart{-kInf, -kInf, 0.0, 0.0, 0.0, 0.0, 0u, 0u};
     const float a = warp_max_nan(fmaxf(p.mr, -kInf)), b = warp_max_nan(fmaxf(p.mr, p.ml));
     // sums below the references (a: outside the list, b: the row)
-    const float za = warp_sum(p.zr != 0.f ? p.zr * ex2((p.mr - a) * c) : 0.f);
-    const float zb = warp_sum((p.zr != 0.f ? p.zr * ex2((p.mr - b) * c) : 0.f) +
-                              (p.zl != 0.f ? p.zl * ex2((p.ml - b) * c) : 0.f));
-    // sum of the teacher's weight times (l - b) c
-    const double su = warp_sum(p.w > 0.0 ? p.wu + p.w * ((static_cast<double>(p.ml) - static_cast<double>(b)) * static_cast<double>(c)) : 0.0);
+    // (the gradient takes them in fp32, the loss in fp64 below)
+    const float zrf = static_cast<float>(p.zr), zlf = static_cast<float>(p.zl);
+    const float za = warp_sum(zrf != 0.f ? zrf * ex2((p.mr - a) * c) : 0.f);
+    const float zb = warp_sum((zrf != 0.f ? zrf * ex2((p.mr - b) * c) : 0.f) + (zlf != 0.f ? zlf * ex2((p.ml - b) * c) : 0.f));
     uint32_t bad = __reduce_or_sync(0xffffffffu, p.bad) | (got ? 0u : 2u);
     if (!(zb > 0.f)) bad |= 1u;  // every logit masked, or NaN
     const bool empty = sh.any == 0u || (!tail && !(sh.s0 > 0.0));
@@ -615,21 +648,28 @@ __global__ void __launch_bounds__(kSThreads, 5) distill_stage_kernel(DistillPara
     }
     __syncwarp();
     if (GRAD) asm volatile("bar.arrive 1, %0;" ::"n"(kSThreads) : "memory");  // the other warps go on with the gradient
-    if (rank == 0 && lane == 0) {
+    if (rank == 0) {
+      const double ad = static_cast<double>(a), bd = static_cast<double>(b);
+      const double zad = warp_sum(p.zr != 0.0 ? p.zr * part_scale(p.mr - a, c, 0.f) : 0.0);
+      const double zld = warp_sum(p.zl != 0.0 ? p.zl * exp2_below((static_cast<double>(p.ml) - bd) * cd) : 0.0);
+      // sum of the teacher's weight times (l - b) c
+      const double su = warp_sum(p.w > 0.0 ? p.wu + p.w * ((static_cast<double>(p.ml) - bd) * cd) : 0.0);
+      const double lz = log2(zld + (zad > 0.0 ? zad * exp2_below((ad - bd) * cd) : 0.0));
       constexpr double kLn2d = 0.69314718055994530942;
       const double norm = tail ? 1.0 : 1.0 / sh.s0;  // a = w * norm
-      const double lz = log2(static_cast<double>(zb));
       double loss = (sh.t1 - sh.s0 * sh.tnorm + kLn2d * (lz * sh.s0 - su)) * norm;
-      if (tail && sh.at > 0.0 && za > 0.f) {
-        const double lq = (static_cast<double>(a) - static_cast<double>(b)) * c + log2(static_cast<double>(za)) - lz;
+      if (tail && sh.at > 0.0 && zad > 0.0) {
+        const double lq = (ad - bd) * cd + log2(zad) - lz;
         loss += sh.at * (log(sh.at) - kLn2d * lq);
       }
-      if (P.loss) P.loss[row] = (!fine || bad) ? __int_as_float(0x7FC00000) : (empty ? 0.f : static_cast<float>(loss));
-      if (P.valid) P.valid[row] = live ? 1 : 0;
-      if (P.status)
-        P.status[row] = sh.status | (sh.dup ? VS_ROW_DUP_SUPPORT_ID : 0u) | (bad & 2u ? VS_ROW_DEVICE_TIMEOUT : 0u) |
-                        (!fine ? VS_ROW_BAD_PARAM : bad ? VS_ROW_NONFINITE_INPUT : empty ? VS_ROW_EMPTY_SUPPORT : 0u);
-      if (P.ctx) static_cast<DistillCtx*>(P.ctx)[row] = sh.k;
+      if (lane == 0) {
+        if (P.loss) P.loss[row] = (!fine || bad) ? __int_as_float(0x7FC00000) : (empty ? 0.f : static_cast<float>(loss));
+        if (P.valid) P.valid[row] = live ? 1 : 0;
+        if (P.status)
+          P.status[row] = sh.status | (sh.dup ? VS_ROW_DUP_SUPPORT_ID : 0u) | (bad & 2u ? VS_ROW_DEVICE_TIMEOUT : 0u) |
+                          (!fine ? VS_ROW_BAD_PARAM : bad ? VS_ROW_NONFINITE_INPUT : empty ? VS_ROW_EMPTY_SUPPORT : 0u);
+        if (P.ctx) static_cast<DistillCtx*>(P.ctx)[row] = sh.k;
+      }
     }
     __syncwarp();
   } else if (GRAD) {

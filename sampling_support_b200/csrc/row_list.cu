@@ -513,8 +513,9 @@ __global__ void __launch_bounds__(kLThreads, 5) list_kernel(const __grid_constan
   {
     auto seen = [&](int g, const Eight<Raw>& v) { two.add(g, max8(v)); };
     if constexpr (Op::kSum) {
-      float m, z;
-      slice_sum(buf, tid, groups, kLThreads, c, m, z, seen);
+      float m, z, rest;
+      slice_sum(buf, tid, groups, kLThreads, c, m, z, rest, seen);
+      z *= ex2(-rest);
       const float wm = warp_max_nan(m);
       z = warp_sum(z != 0.f ? z * ex2((m - wm) * c) : 0.f);
       if (lane == 0) sh.red[warp] = make_float2(wm, z);

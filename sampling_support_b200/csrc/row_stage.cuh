@@ -167,7 +167,7 @@ __device__ __forceinline__ void push_words(uint32_t dst, uint32_t bar, const voi
 // z = sum of 2^((l - m) c) below a reference m.  The first group's maximum
 // serves as long as the sum stays moderate (a sum of powers of two keeps its
 // relative precision whatever the reference), which saves a pass; one fused
-// multiply-add per exponent, the rounding of m c put back after.  Masked
+// multiply-add per exponent, from m c rounded: the sum is z 2^-rest.  Masked
 // first groups, far larger values later, and l c that overflows take the
 // thread's maximum and the differences first.  A NaN or +inf comes out as m.
 // seen(g, group g) runs once for every group when it is given.
@@ -177,10 +177,10 @@ struct SeenNone {
 };
 template <typename Raw, typename Seen = SeenNone>
 __device__ __forceinline__ void slice_sum(const Raw* buf, int g0, int groups, int step, float c, float& m, float& z,
-                                          Seen&& seen = Seen{}) {
+                                          float& rest, Seen&& seen = Seen{}) {
   constexpr bool kSeen = !std::is_same_v<std::decay_t<Seen>, SeenNone>;
   m = -kInf;
-  z = 0.f;
+  z = rest = 0.f;
   if (g0 >= groups) return;
   {
     Eight<Raw> v;
@@ -214,10 +214,11 @@ __device__ __forceinline__ void slice_sum(const Raw* buf, int g0, int groups, in
     }
     float a, b;
     unpack2(add2(z2, y2), a, b);
-    z = (a + b) * ex2(-fmaf(m, c, -mc));
+    z = a + b;
+    rest = fmaf(m, c, -mc);
   }
   if (z > 0.f && z < 1e30f) return;
-  z = 0.f;
+  z = rest = 0.f;
   m = -kInf;
   for (int g = g0; g < groups; g += step) {
     Eight<Raw> v;
