@@ -246,18 +246,18 @@ inline int stage_cluster_size(int rows, int vocab, int esize) {
   return (bytes + c - 1) / c <= (200 << 10) ? c : 0;
 }
 
-// Lets `kernel` use `bytes` of dynamic shared memory on the current device,
-// once per device and size that grows (the attribute call costs about as much
-// host time as the launch).
+// Lets `kernel` use all of an SM's dynamic shared memory on the current device,
+// once per device (the attribute call costs about as much host time as the
+// launch).  All of it, not what one call needs: threads that set different
+// sizes could take each other's grant back before the launch.
 template <typename K>
-cudaError_t allow_shared(K kernel, size_t bytes, std::atomic<int> (&granted)[64]) {
+cudaError_t allow_shared(K kernel, std::atomic<bool> (&granted)[64]) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
-  const int want = static_cast<int>(bytes);
-  if (dev < 64 && granted[dev].load(std::memory_order_relaxed) >= want) return cudaSuccess;
-  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, want);
-  if (e == cudaSuccess && dev < 64) granted[dev].store(want, std::memory_order_relaxed);
+  if (dev < 64 && granted[dev].load(std::memory_order_relaxed)) return cudaSuccess;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 << 10);
+  if (e == cudaSuccess && dev < 64) granted[dev].store(true, std::memory_order_relaxed);
   return e;
 }
 
@@ -266,8 +266,8 @@ cudaError_t allow_shared(K kernel, size_t bytes, std::atomic<int> (&granted)[64]
 template <auto Kernel, typename... Args>
 cudaError_t launch_cluster(unsigned grid, int c, int threads, size_t smem, bool behind, cudaStream_t s,
                            const Args&... args) {
-  static std::atomic<int> granted[64];
-  const cudaError_t e = allow_shared(Kernel, smem, granted);
+  static std::atomic<bool> granted[64];
+  const cudaError_t e = allow_shared(Kernel, granted);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(grid);

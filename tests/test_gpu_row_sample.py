@@ -239,6 +239,7 @@ def test_calls_at_once_from_two_threads():
     import threading
 
     x = [logits_on("cuda", rows, 60_000, dtype, seed=16) for rows, dtype in ((3, BF), (20, F32))]
+    y = [t.to(BF) for t in x]
     u = [numbers(3, 10), numbers(20, 11)]
     kw = [dict(top_p=0.9), dict(top_k=30)]
     torch.cuda.synchronize()
@@ -248,7 +249,7 @@ def test_calls_at_once_from_two_threads():
         stream = torch.cuda.Stream()
         for _ in range(40):
             outs[i].append(vsb.sample(x[i], u[i], stream=stream, **kw[i]))
-            outs[i].append(vsb.topk_logprob(x[i], 50, stream=stream))
+            outs[i].append(vsb.topk_logprob(y[i], (50, 900)[i], stream=stream))  # of different shared memory
         stream.synchronize()
 
     threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
