@@ -524,7 +524,7 @@ __device__ __forceinline__ void sample_row(const SampleParams& P, int row) {
 }
 
 // One cluster per row, one CTA per SM.  Measured (device time): 128 x 151,936
-// bf16 with top-p 37 us, 512 of them 116 us (1.3 TB/s), 64 x 151,936 fp32 over
+// bf16 with top-p 37 us, 512 with mixed filters 116 us (1.3 TB/s), 64 x 151,936 fp32 over
 // the whole vocabulary 64 us.  A bf16 row is bound by its one shared atomic per
 // element and by the latency of what follows it (reduction, decision, the
 // token among its equals, about 12 us); an fp32 row by its masses pass (24 us
