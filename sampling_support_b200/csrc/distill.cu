@@ -403,17 +403,19 @@ struct alignas(16) DistillPart {
 };
 static_assert(sizeof(DistillPart) == 48, "three 16-byte words");
 
-// 2^x for x <= 0 to 3e-10 of itself (0 below 2^-1000): the Taylor polynomial of
+// 2^x for |x| <= 1,000 to 3e-10 of itself: the Taylor polynomial of
 // degree 8 in the fraction, in pairs, a shorter chain than exp2()'s; the list's
 // warp is as long as the slice's passes.
-__device__ __forceinline__ double exp2_below(double x) {
+__device__ __forceinline__ double exp2_near(double x) {
   const double r = x + 6755399441055744.0;  // 1.5 * 2^52: the integer lands in the low word
   const double f = (x - (r - 6755399441055744.0)) * 0.69314718055994531, f2 = f * f;
   const double lo = fma(f2, fma(f, 1.0 / 6.0, 0.5), 1.0 + f);
   const double hi = fma(f2, fma(f2, 1.0 / 40320.0, fma(f, 1.0 / 5040.0, 1.0 / 720.0)), fma(f, 1.0 / 120.0, 1.0 / 24.0));
   const double p = fma(f2 * f2, hi, lo);
-  return x >= -1000.0 ? __hiloint2double(__double2hiint(p) + (__double2loint(r) << 20), __double2loint(p)) : 0.0;
+  return __hiloint2double(__double2hiint(p) + (__double2loint(r) << 20), __double2loint(p));
 }
+// The same for any x <= 0, 0 where it is small.
+__device__ __forceinline__ double exp2_below(double x) { return x >= -1000.0 ? exp2_near(x) : 0.0; }
 
 // 2^(d c - rest) for a part's distance d <= 0 from the largest: the product's
 // rounding is put back (at d = -20 it would be worth 1e-6), what is left is the
@@ -564,7 +566,6 @@ __global__ void __launch_bounds__(kSThreads, 5) distill_stage_kernel(DistillPara
     double s0 = 0.0, t1 = 0.0, ws = 0.0, wu = 0.0;
     uint32_t bad = lmax < kInf ? 0u : 1u;  // NaN or +inf
     double zl = 0.0;
-#pragma unroll 1
     for (int s = lane; s < W; s += 32) {
       const int id = ids[s];
       if (id < 0) continue;
@@ -572,7 +573,8 @@ __global__ void __launch_bounds__(kSThreads, 5) distill_stage_kernel(DistillPara
       const bool own = id >= j0 && id < j1;
       bad |= !(l < kInf) ? 1u : 0u;
       if (l > -kInf) {
-        const double w = exp(static_cast<double>(l) - static_cast<double>(off));
+        const double below = static_cast<double>(l) - static_cast<double>(off), x2 = below * 1.4426950408889634;
+        const double w = fabs(x2) <= 1000.0 ? exp2_near(x2) : exp(below);
         s0 += w;
         t1 += w * static_cast<double>(l);
         if (own && w > 0.0) {
