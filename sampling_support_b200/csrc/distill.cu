@@ -417,9 +417,11 @@ __device__ __forceinline__ double exp2_near(double x) {
 // The same for any x <= 0, 0 where it is small.
 __device__ __forceinline__ double exp2_below(double x) { return x >= -1000.0 ? exp2_near(x) : 0.0; }
 
-// 2^(d c - rest) for a part's distance d <= 0 from the largest: the product's
-// rounding is put back (at d = -20 it would be worth 1e-6), what is left is the
-// exponential's 2^-22, and nothing at d = 0, where most of the mass is.
+// 2^(d c - rest) for a part's distance d <= 0 from the largest, |rest| at most
+// 2^-13 (slice_sum): the product's rounding is put back (at d = -20 it would be
+// worth 1e-6) and so is rest, both to first order.  What is left is the exponential's
+// 2^-22, and nothing at d = 0; d is a distance of references, each the maximum of
+// a thread's first group, so a part below the largest may hold much of the mass.
 __device__ __forceinline__ double part_scale(float d, float c, float rest) {
   const float p = __fmul_rn(d, c);
   const float lo = fmaf(d, c, -p) - rest;

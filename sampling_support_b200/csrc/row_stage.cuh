@@ -167,10 +167,14 @@ __device__ __forceinline__ void push_words(uint32_t dst, uint32_t bar, const voi
 // z = sum of 2^((l - m) c) below a reference m.  The first group's maximum
 // serves as long as the sum stays moderate (a sum of powers of two keeps its
 // relative precision whatever the reference), which saves a pass; one fused
-// multiply-add per exponent, from m c rounded: the sum is z 2^-rest.  Masked
-// first groups, far larger values later, and l c that overflows take the
-// thread's maximum and the differences first.  A NaN or +inf comes out as m.
-// seen(g, group g) runs once for every group when it is given.
+// multiply-add per exponent, from m c rounded: the sum is z 2^-rest.  That
+// holds for |m c| below kDirect (logits over T up to 2,839), where |rest| is at
+// most 2^-13 and a caller may put it back to first order: the square is worth
+// 4e-9.  Beyond (small T, common offsets, masks by a finite value) rest would
+// reach whole powers of two: there, after masked first groups and before far
+// larger values the thread's maximum and the differences come first.  A NaN or
+// +inf comes out as m.  seen(g, group g) runs once for every group when it is given.
+constexpr float kDirect = 4096.f;
 struct SeenNone {
   template <typename T>
   __device__ __forceinline__ void operator()(int, const T&) const {}
@@ -188,7 +192,7 @@ __device__ __forceinline__ void slice_sum(const Raw* buf, int g0, int groups, in
     m = max8(v);
   }
   const float mc = __fmul_rn(m, c);
-  const bool direct = fabsf(mc) < 1e37f;
+  const bool direct = fabsf(mc) < kDirect;
   if (kSeen && !direct)
     for (int g = g0; g < groups; g += step) {
       Eight<Raw> v;

@@ -1,0 +1,157 @@
+"""vs_distill_fwd / vs_distill_bwd over the whole range of their inputs: masks
+by a finite value, logits with a common offset, small and large temperatures,
+teacher values of any size, almost all of the teacher's mass on the list, a
+loss near zero.
+
+The bounds.  The factor log2(e) / T is rounded to fp32 (a relative d of at most
+2^-23); logits are subtracted before they are multiplied, or the product's
+rounding is put back, so
+
+* loss: d moves log q_k by d |z_k - E z|; the a-weighted sum of those distances
+  is at most the loss, plus the entropies (log 1,024, log of the vocabulary:
+  below 30 together).  The normaliser's fp32 exponentials are worth at most
+  1.5e-5 (2^-22 each, 2^-23 of an argument of at most 60, 2^-24 for each of at
+  most 96 additions), the tail's the same.  With the rounding of the result,
+  |error| <= 4e-5 + 2^-22 |loss|.
+* gradient of element j, over g / T: q_j and a_j relative to themselves by the
+  normaliser's 1e-5 and by d |z_j - z_max| <= 2^-23 * 87 = 1e-5 (beyond 87 nats
+  q_j is below 2^-125): 2e-5 in all; outside the list the same of the product
+  r_j (q_t - a_t); the stored value by half a step of its type."""
+
+import numpy as np
+import pytest
+import torch
+
+import sampling_support_b200 as vsb
+from _row_ops import logits_on, widen
+
+pytestmark = pytest.mark.gpu
+
+BF, F32 = torch.bfloat16, torch.float32
+
+
+def two_calls(x, ids, lp, t, tail, vocab, grad_dtype, g):
+    """(loss, valid, status, gradient) of a forward and a backward call."""
+    kw = dict(temperature=t, tail=tail, vocab=vocab)
+    out = vsb.distill_fwd(x, ids, lp, want_grad=True, **kw)
+    grad = vsb.distill_bwd(x, ids, lp, out["ctx"], g, grad_dtype=grad_dtype, **kw)
+    return out["loss"], out["valid"], out["status"], grad[:, :vocab]
+
+
+def log_sum(z):
+    top = z.max()
+    return top + np.log(np.exp(z - top).sum())
+
+
+def plain_row(x, ids, lp, t, tail):
+    """(loss, valid, gradient, q, a over the vocabulary) of a row without masked tokens whose list has different
+    ids in the vocabulary; a share far below fp64's range keeps its logarithm."""
+    with np.errstate(over="ignore"):
+        z = x / t
+    z = z - z.max()
+    logq = z - log_sum(z)
+    lp = lp.astype(np.float64)
+    la = lp if tail else lp - log_sum(lp)
+    a = np.exp(la)
+    loss = float((a * (la - logq[ids])).sum())
+    full = np.zeros(len(x))
+    full[ids] = a
+    q = np.exp(logq)
+    grad = q - full
+    off = np.ones(len(x), bool)
+    off[ids] = False
+    if tail and off.any():
+        rest, log_qt = max(0.0, 1.0 - a.sum()), log_sum(logq[off])
+        if rest > 0:
+            loss += rest * (np.log(rest) - log_qt)
+        r = np.exp(z[off] - z[off].max())
+        grad[off] = r / r.sum() * (np.exp(log_qt) - rest)
+    return loss, 1, grad / t, q, full
+
+
+WAYS = [two_calls]
+
+
+def check(x, ids, lp, t, tail, vocab, grad_dtype=F32, g=1.0):
+    xs, li, ll = widen(x[:, :vocab]), ids.cpu().numpy(), lp.cpu().numpy()
+    gs = torch.full((len(x),), g, device="cuda")
+    ways = [f(x, ids, lp, t, tail, vocab, grad_dtype, gs) for f in WAYS]
+    torch.cuda.synchronize()
+    tr, gr = float(np.float32(t)), float(np.float32(g))
+    half = torch.finfo(grad_dtype).eps / 2
+    for r in range(len(xs)):
+        want, ok, d, q, a = plain_row(xs[r], li[r], ll[r], tr, tail)
+        d = d * gr
+        tol = 2e-5 * gr / tr * (q + a) + 2e-5 * np.abs(d) + half * np.abs(d) * (1 + 1e-4) + 1e-37
+        for way, (loss, valid, status, grad) in zip([f.__name__ for f in WAYS], ways):
+            assert int(valid[r]) == ok and int(status[r]) == 0, (way, r)
+            got = float(loss[r])
+            assert abs(got - want) <= 4e-5 + 2.0 ** -22 * abs(want), (way, r, got, want)
+            off = np.abs(widen(grad[r]) - d) - tol
+            worst = int(np.argmax(np.where(np.isnan(off), np.inf, off)))
+            assert off[worst] <= 0, (way, r, worst, float(grad[r, worst]), d[worst])
+
+
+def listed(rows, vocab, k, seed):
+    """k different ids per row and log-probabilities that leave about a fifth of the mass."""
+    g = torch.Generator().manual_seed(seed)
+    ids = torch.stack([torch.randperm(vocab, generator=g)[:k] for _ in range(rows)]).to(torch.int32)
+    lp = torch.log(0.8 * torch.softmax(torch.randn((rows, k), generator=g), 1))
+    return ids, lp
+
+
+MASKS = [-1e4, -1e6, -1e7, -1e9, -1e10, -1e14, -1e30]
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("tail", [False, True])
+@pytest.mark.parametrize("mask", MASKS)
+@pytest.mark.parametrize("vocab", [1003, 20_011])
+def test_finite_masks(dtype, tail, mask, vocab):
+    """Constrained decoding with a finite mask: every token off the list masked,
+    most of them, the whole row, and listed tokens too."""
+    rows, k = 4, 20
+    x = logits_on("cpu", rows, vocab, F32, seed=vocab, ld=vocab + (-vocab) % 8)
+    ids, lp = listed(rows, vocab, k, seed=31)
+    on = torch.zeros((rows, x.shape[1]), dtype=torch.bool).scatter_(1, ids.long(), True)
+    some = torch.rand((rows, x.shape[1]), generator=torch.Generator().manual_seed(32)) < 0.9
+    x[0] = torch.where(on[0], x[0], torch.tensor(mask))
+    x[1] = torch.where(~on[1] & some[1], torch.tensor(mask), x[1])
+    x[2] = mask
+    x[3] = torch.where(some[3], torch.tensor(mask), x[3])
+    check(x.to(dtype).cuda(), ids.cuda(), lp.cuda(), 1.0, tail, vocab, dtype)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_finite_masks_of_the_largest_vocabularies(dtype):
+    rows, vocab, k = 2, 1 << 20, 20
+    x = logits_on("cpu", rows, vocab, F32, seed=3)
+    ids, lp = listed(rows, vocab, k, seed=33)
+    on = torch.zeros((rows, vocab), dtype=torch.bool).scatter_(1, ids.long(), True)
+    x[0] = torch.where(on[0], x[0], torch.tensor(-1e9))
+    x[1, ::2] = -1e9
+    check(x.to(dtype).cuda(), ids.cuda(), lp.cuda(), 1.0, True, vocab, dtype)
+
+
+@pytest.mark.parametrize("tail", [False, True])
+@pytest.mark.parametrize("offset", [1e3, -1e4, 1e6, -1e6, 1e7])
+@pytest.mark.parametrize("vocab", [1003, 20_011])
+def test_common_offsets(tail, offset, vocab):
+    x = logits_on("cuda", 3, vocab, F32, seed=7) + offset
+    ids, lp = listed(3, vocab, 30, seed=34)
+    check(x, ids.cuda(), lp.cuda(), 1.0, tail, vocab)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("tail", [False, True])
+@pytest.mark.parametrize("t", [1e-2, 1e-3, 1e-5, 1e-6, 1e-9, 1e-12])
+@pytest.mark.parametrize("vocab", [1003, 20_011])
+def test_small_temperatures(dtype, tail, t, vocab):
+    """The row's largest token on the list, off it, and shared by both."""
+    x = logits_on("cuda", 3, vocab, dtype, seed=8, spikes=0)
+    ids, lp = listed(3, vocab, 30, seed=35)
+    x[0, int(ids[0, 3])] = 14.0
+    out = next(j for j in range(500, vocab) if j not in ids[1].tolist())
+    x[1, out] = 14.0
+    x[2, int(ids[2, 0])] = x[2, next(j for j in range(700, vocab) if j not in ids[2].tolist())] = 14.0
+    check(x, ids.cuda(), lp.cuda(), t, tail, vocab)
