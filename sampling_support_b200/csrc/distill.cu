@@ -686,10 +686,11 @@ __global__ void __launch_bounds__(kSThreads, 5) distill_stage_kernel(DistillPara
     G* out = static_cast<G*>(P.dlogits) + static_cast<int64_t>(row) * P.grad_ld;
     const float scale = k.zero ? 0.f : (P.g_loss ? P.g_loss[row] : 1.f) * k.inv_t;
     const float dense = scale * k.coef;
-    // one fused multiply-add per exponent: l c - (ref c + lz), the constant's rounding in the factor
+    // one fused multiply-add per exponent: l c - (ref c + lz), the constant's rounding in the factor (at most
+    // 2^(1/32): a larger constant's would overflow it, and there the differences come first)
     const double shift = static_cast<double>(k.ref) * k.c + static_cast<double>(k.lz);
     const float sf = static_cast<float>(shift);
-    const bool wide = !(fabsf(sf) < 1e37f);  // l c may overflow: the differences first
+    const bool wide = !(fabsf(sf) < 1048576.f);
     const float lead = wide ? dense : dense * exp2f(static_cast<float>(static_cast<double>(sf) - shift));
     const f32x2 c2 = pack2(k.c, k.c), s2 = pack2(-sf, -sf), d2 = pack2(lead, lead);
     for (int g = tid; g < groups; g += kSThreads) {
