@@ -37,8 +37,8 @@ constexpr int kBThreads = 256;  // backward kernel
 struct alignas(16) DistillCtx {
   float c;      // log2(e) / T
   float inv_t;  // 1 / T
-  // an element's share is 2^((l - ref) c - lz): the differences of the logits come first, so that
-  // l c may overflow (rows at the type's lowest value)
+  // an element's share is 2^((l - ref) c - lz): the differences of the logits come first (halved, with
+  // twice the factor), so that l c and l - ref may overflow (rows at the type's ends)
   float ref, lz;    // of the dense part: the whole row's, or what lies outside the list
   float coef;       // factor of the dense part: 1, or q_t - a_t
   float rall, lall; // the whole row's
@@ -75,7 +75,7 @@ __device__ __forceinline__ void grad_pass(const Raw* __restrict__ row, G* __rest
                                           const DistillCtx& k, float g, const int32_t* ids, const float* lp,
                                           int width) {
   const float scale = k.zero ? 0.f : g * k.inv_t;
-  const float dense = scale * k.coef;
+  const float dense = scale * k.coef, c2 = 2.f * k.c;
   // what the listed elements held before the accumulation
   constexpr int SLOTS = (VS_MAX_SUPPORT_WIDTH + NT - 1) / NT;
   float old[SLOTS];
@@ -96,14 +96,14 @@ __device__ __forceinline__ void grad_pass(const Raw* __restrict__ row, G* __rest
       if constexpr (ACC) o.load(out + j);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        float d = k.zero ? 0.f : dense * ex2(fmaf(value_of(x.e[i]) - k.ref, k.c, -k.lz));
+        float d = k.zero ? 0.f : dense * ex2(fmaf(half_diff(value_of(x.e[i]), k.ref), c2, -k.lz));
         if constexpr (ACC) d += grad_value(o.e[i]);
         o.e[i] = to_grad<G>(d);
       }
       o.store(out + j);
     } else {
       for (int i = j; i < j1; ++i) {
-        float d = k.zero ? 0.f : dense * ex2(fmaf(value_of(row[i]) - k.ref, k.c, -k.lz));
+        float d = k.zero ? 0.f : dense * ex2(fmaf(half_diff(value_of(row[i]), k.ref), c2, -k.lz));
         if constexpr (ACC) d += grad_value(out[i]);
         out[i] = to_grad<G>(d);
       }
@@ -116,7 +116,7 @@ __device__ __forceinline__ void grad_pass(const Raw* __restrict__ row, G* __rest
     const int s = threadIdx.x + i * NT;
     const int id = s < width ? ids[s] : -1;
     if (id >= j0 && id < j1 && (!k.dup || first_of(ids, s))) {
-      const float q = ex2(fmaf(value_of(row[id]) - k.rall, k.c, -k.lall));
+      const float q = ex2(fmaf(half_diff(value_of(row[id]), k.rall), c2, -k.lall));
       float d = scale * (q - expf(lp[s] - k.tnorm));
       if constexpr (ACC) d += old[i];
       out[id] = to_grad<G>(d);
@@ -180,7 +180,7 @@ struct Online {
 #pragma unroll
     for (int i = 1; i < 8; ++i) t = fmaxf(t, x[i]);
     if (t > v) {
-      z = v == -kInf ? 0.f : z * ex2((v - t) * c);
+      z = v == -kInf ? 0.f : z * ex2(half_diff(v, t) * (2.f * c));
       v = t;
     }
     if (v == -kInf) {  // nothing but masked elements so far, or NaN
@@ -190,7 +190,7 @@ struct Online {
     }
     float s = 0.f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) s += ex2((x[i] - v) * c);
+    for (int i = 0; i < 8; ++i) s += ex2(half_diff(x[i], v) * (2.f * c));
     z += s;
   }
 };
@@ -210,7 +210,7 @@ __global__ void __launch_bounds__(kDThreads) distill_fwd_kernel(DistillParams P)
   const int j0 = min(V, rank * P.chunk), j1 = min(V, j0 + P.chunk);
   const float t = P.temperature ? P.temperature[row] : P.temperature_scalar;
   const bool fine = t >= kLeastT && t < kInf;
-  const float c = fminf(kLog2e / t, 3e38f);
+  const float c = exponent_factor(t);
 
   // the list: marks over the whole vocabulary, repeats found on the way
   const int words = (V + 31) / 32;
@@ -417,14 +417,14 @@ __device__ __forceinline__ double exp2_near(double x) {
 // The same for any x <= 0, 0 where it is small.
 __device__ __forceinline__ double exp2_below(double x) { return x >= -1000.0 ? exp2_near(x) : 0.0; }
 
-// 2^(d c - rest) for a part's distance d <= 0 from the largest, |rest| at most
+// 2^(d c - rest) for a part's distance d = x - ref <= 0 from the largest, |rest| at most
 // 2^-13 (slice_sum): the product's rounding is put back (at d = -20 it would be
 // worth 1e-6) and so is rest, both to first order.  What is left is the exponential's
 // 2^-22, and nothing at d = 0; d is a distance of references, each the maximum of
 // a thread's first group, so a part below the largest may hold much of the mass.
-__device__ __forceinline__ double part_scale(float d, float c, float rest) {
-  const float p = __fmul_rn(d, c);
-  const float lo = fmaf(d, c, -p) - rest;
+__device__ __forceinline__ double part_scale(float x, float ref, float c, float rest) {
+  const float d = half_diff(x, ref), c2 = 2.f * c, p = __fmul_rn(d, c2);
+  const float lo = fmaf(d, c2, -p) - rest;
   const float e = ex2(p);
   return e > 0.f ? static_cast<double>(e) * (1.0 + 0.69314718055994531 * static_cast<double>(lo)) : 0.0;
 }
@@ -493,7 +493,7 @@ __global__ void __launch_bounds__(kSThreads, 5) distill_stage_kernel(DistillPara
   asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");  // ordered by the fence above
   const float t = P.temperature ? P.temperature[row] : P.temperature_scalar;
   const bool fine = t >= kLeastT && t < kInf;
-  const float c = fminf(kLog2e / t, 3e38f);
+  const float c = exponent_factor(t);
   const bool tail = P.tail != 0;
   for (int i = n / 8 * 8 + tid; i < groups * 8; i += kSThreads) buf[i] = i < n ? x[j0 + i] : kMasked;
 
@@ -603,7 +603,7 @@ __global__ void __launch_bounds__(kSThreads, 5) distill_stage_kernel(DistillPara
     float m, z, rest;
     slice_sum(buf, tid - 32, groups, kSSlice, c, m, z, rest);
     const float wm = warp_max_nan(m);  // a NaN or +inf marks the part
-    const double zw = warp_sum(z != 0.f ? z * part_scale(m - wm, c, rest) : 0.0);
+    const double zw = warp_sum(z != 0.f ? z * part_scale(m, wm, c, rest) : 0.0);
     if (lane == 0) {
       sh.red_m[tid >> 5] = wm;
       sh.red_z[tid >> 5] = zw;
@@ -616,7 +616,7 @@ __global__ void __launch_bounds__(kSThreads, 5) distill_stage_kernel(DistillPara
     const float m = in ? sh.red_m[lane] : -kInf;
     const double z = in ? sh.red_z[lane] : 0.0;
     mine.mr = warp_max_nan(m);
-    mine.zr = warp_sum(z != 0.0 ? z * part_scale(m - mine.mr, c, 0.f) : 0.0);
+    mine.zr = warp_sum(z != 0.0 ? z * part_scale(m, mine.mr, c, 0.f) : 0.0);
     mine.bad |= sh.bad | (mine.mr < kInf ? 0u : 1u);
     if (lane < (GRAD ? C : 1)) push_words<sizeof(DistillPart) / 16>(peer_addr(&sh.parts[rank], lane), peer_addr(&sh.xbar, lane), &mine);
   }
@@ -631,8 +631,10 @@ __global__ void __launch_bounds__(kSThreads, 5) distill_stage_kernel(DistillPara
     // sums below the references (a: outside the list, b: the row)
     // (the gradient takes them in fp32, the loss in fp64 below)
     const float zrf = static_cast<float>(p.zr), zlf = static_cast<float>(p.zl);
-    const float za = warp_sum(zrf != 0.f ? zrf * ex2((p.mr - a) * c) : 0.f);
-    const float zb = warp_sum((zrf != 0.f ? zrf * ex2((p.mr - b) * c) : 0.f) + (zlf != 0.f ? zlf * ex2((p.ml - b) * c) : 0.f));
+    const float c2 = 2.f * c;
+    const float za = warp_sum(zrf != 0.f ? zrf * ex2(half_diff(p.mr, a) * c2) : 0.f);
+    const float zb = warp_sum((zrf != 0.f ? zrf * ex2(half_diff(p.mr, b) * c2) : 0.f) +
+                              (zlf != 0.f ? zlf * ex2(half_diff(p.ml, b) * c2) : 0.f));
     uint32_t bad = __reduce_or_sync(0xffffffffu, p.bad) | (got ? 0u : 2u);
     if (!(zb > 0.f)) bad |= 1u;  // every logit masked, or NaN
     const bool empty = sh.any == 0u || (!tail && !(sh.s0 > 0.0));
@@ -646,7 +648,7 @@ __global__ void __launch_bounds__(kSThreads, 5) distill_stage_kernel(DistillPara
       k.lall = log2f(zb);
       k.ref = outside ? a : b;
       k.lz = outside ? log2f(za) : k.lall;
-      k.coef = tail ? (outside ? static_cast<float>(static_cast<double>(exp2f((a - b) * c) * za / zb) - sh.at) : 0.f) : 1.f;
+      k.coef = tail ? (outside ? static_cast<float>(static_cast<double>(exp2f(half_diff(a, b) * c2) * za / zb) - sh.at) : 0.f) : 1.f;
       k.tnorm = static_cast<float>(sh.tnorm);
       k.zero = live ? 0u : 1u;
       k.dup = sh.dup;
@@ -656,7 +658,7 @@ __global__ void __launch_bounds__(kSThreads, 5) distill_stage_kernel(DistillPara
     if (GRAD) asm volatile("bar.arrive 1, %0;" ::"n"(kSThreads) : "memory");  // the other warps go on with the gradient
     if (rank == 0) {
       const double ad = static_cast<double>(a), bd = static_cast<double>(b);
-      const double zad = warp_sum(p.zr != 0.0 ? p.zr * part_scale(p.mr - a, c, 0.f) : 0.0);
+      const double zad = warp_sum(p.zr != 0.0 ? p.zr * part_scale(p.mr, a, c, 0.f) : 0.0);
       const double zld = warp_sum(p.zl != 0.0 ? p.zl * exp2_below((static_cast<double>(p.ml) - bd) * cd) : 0.0);
       // sum of the teacher's weight times (l - b) c
       const double su = warp_sum(p.w > 0.0 ? p.wu + p.w * ((static_cast<double>(p.ml) - bd) * cd) : 0.0);
@@ -706,7 +708,7 @@ __global__ void __launch_bounds__(kSThreads, 5) distill_stage_kernel(DistillPara
       if (k.zero || wide) {
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-          d[i] = k.zero ? 0.f : dense * ex2(fmaf(value_of(v.e[i]) - k.ref, k.c, -k.lz));
+          d[i] = k.zero ? 0.f : dense * ex2(fmaf(half_diff(value_of(v.e[i]), k.ref), 2.f * k.c, -k.lz));
       }
       const int j = j0 + g * 8;
       if (j + 8 <= j1) {
@@ -725,7 +727,7 @@ __global__ void __launch_bounds__(kSThreads, 5) distill_stage_kernel(DistillPara
       for (int s = tid; s < W; s += kSThreads) {
         const int id = ids[s];
         if (id >= j0 && id < j1)
-          out[id] = to_grad<G>(scale * (ex2(fmaf(us[s] - k.rall, k.c, -k.lall)) - expf(lps[s] - k.tnorm)));
+          out[id] = to_grad<G>(scale * (ex2(fmaf(half_diff(us[s], k.rall), 2.f * k.c, -k.lall)) - expf(lps[s] - k.tnorm)));
       }
   }
 }

@@ -249,7 +249,8 @@ struct TopkOp {
       const bool in = static_cast<uint32_t>(i) < nk;
       const u64 e = in ? sorted[i] : 0ull;
       ids[i] = in ? static_cast<int32_t>(~static_cast<uint32_t>(e)) : -1;
-      if (lps) lps[i] = in ? (KeyTraits<Raw>::decode(static_cast<uint32_t>(e >> 32)) - vmax) / t - lz : -kInf;
+      if (lps)
+        lps[i] = in ? 2.f * (half_diff(KeyTraits<Raw>::decode(static_cast<uint32_t>(e >> 32)), vmax) / t) - lz : -kInf;
     }
     if (threadIdx.x == 0 && P.status) P.status[row] = 0u;
   }
@@ -504,7 +505,7 @@ __global__ void __launch_bounds__(kLThreads, 5) list_kernel(const __grid_constan
   }
   if (tid >= 64 && tid < 64 + kLPush) sh.mine.e[tid - 64] = 0ull;
   const bool fine = Op::fine(P, row);
-  const float t = Op::t_of(P, row), c = fminf(kLog2e / t, 3e38f);
+  const float t = Op::t_of(P, row), c = exponent_factor(t);
   cta_sync();
   if (bytes && !mbar_wait(&sh.bar, 0)) atomicOr(&sh.bad, 1u);
   __syncwarp();
@@ -519,7 +520,7 @@ __global__ void __launch_bounds__(kLThreads, 5) list_kernel(const __grid_constan
       slice_sum(buf, tid, groups, kLThreads, c, m, z, rest, seen);
       z *= ex2(-rest);
       const float wm = warp_max_nan(m);
-      z = warp_sum(z != 0.f ? z * ex2((m - wm) * c) : 0.f);
+      z = warp_sum(z != 0.f ? z * ex2(half_diff(m, wm) * (2.f * c)) : 0.f);
       if (lane == 0) sh.red[warp] = make_float2(wm, z);
     } else {
       for (int g = tid; g < groups; g += kLThreads) {
@@ -600,7 +601,7 @@ __global__ void __launch_bounds__(kLThreads, 5) list_kernel(const __grid_constan
     if constexpr (Op::kSum) {
       const float2 r = lane < kLWarps ? sh.red[lane] : make_float2(-kInf, 0.f);
       part.m = warp_max_nan(r.x);
-      part.z = warp_sum(r.y != 0.f ? r.y * ex2((r.x - part.m) * c) : 0.f);
+      part.z = warp_sum(r.y != 0.f ? r.y * ex2(half_diff(r.x, part.m) * (2.f * c)) : 0.f);
     }
     if (lane < C)
       push_words<sizeof(ListPart) / 16>(peer_addr(&sh.parts[rank], lane), peer_addr(&sh.xbar, lane), &part);
@@ -691,7 +692,7 @@ __global__ void __launch_bounds__(kLThreads, 5) list_kernel(const __grid_constan
   u64* sorted = list_sort(list, spare, total, nk, sh);
   float z = 0.f;
   if constexpr (Op::kSum)
-    z = warp_sum(lane < C && p.z != 0.f ? p.z * ex2((p.m - vmax) * c) : 0.f);
+    z = warp_sum(lane < C && p.z != 0.f ? p.z * ex2(half_diff(p.m, vmax) * (2.f * c)) : 0.f);
   Op::template finish<Raw>(P, row, sorted, sorted == list ? spare : list, nk, vmax, z);
 }
 

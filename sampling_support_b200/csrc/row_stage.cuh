@@ -163,6 +163,14 @@ __device__ __forceinline__ void push_words(uint32_t dst, uint32_t bar, const voi
         : "memory");
 }
 
+// Half of x - ref.  The difference itself may leave fp32 (logits at both ends of
+// the type) where the difference over T does not; halving is exact, one rounding
+// as for the difference, and the factor behind it doubles.
+__device__ __forceinline__ float half_diff(float x, float ref) { return fmaf(0.5f, x, -0.5f * ref); }
+
+// log2(e) / T, for T >= 2^-126 below 2^127: twice of it is finite.
+__device__ __forceinline__ float exponent_factor(float t) { return fminf(kLog2e / t, 1.5e38f); }
+
 // A thread's share of a staged slice, the groups of eight g0, g0 + step, ..:
 // z = sum of 2^((l - m) c) below a reference m.  The first group's maximum
 // serves as long as the sum stays moderate (a sum of powers of two keeps its
@@ -234,7 +242,7 @@ __device__ __forceinline__ void slice_sum(const Raw* buf, int g0, int groups, in
       Eight<Raw> v;
       v.load(buf + g * 8);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) z += ex2((value_of(v.e[i]) - m) * c);
+      for (int i = 0; i < 8; ++i) z += ex2(half_diff(value_of(v.e[i]), m) * (2.f * c));
     }
 }
 

@@ -668,12 +668,12 @@ __device__ __forceinline__ void topk_row(const TopkParams& P, int row) {
 
   // sum of 2^((l - max) log2(e) / T): fp32 per thread, fixed order across
   // the threads and the cluster
-  const float c = kLog2e / t;
+  const float c2 = 2.f * exponent_factor(t);
   if (lps) {
     float z = 0.f;
     R.each([&](int, const auto& r) {
 #pragma unroll
-      for (int i = 0; i < RsRow<Raw>::VEC; ++i) z += ex2((value_of(r[i]) - vmax) * c);
+      for (int i = 0; i < RsRow<Raw>::VEC; ++i) z += ex2(half_diff(value_of(r[i]), vmax) * c2);
     });
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
@@ -702,7 +702,8 @@ __device__ __forceinline__ void topk_row(const TopkParams& P, int row) {
       const u64 e = in ? sh.sorted[i] : 0ull;
       ids[i] = in ? static_cast<int32_t>(~static_cast<uint32_t>(e)) : -1;
       if (lps)
-        lps[i] = in ? (KeyTraits<Raw>::decode(static_cast<uint32_t>(e >> 32)) - vmax) / t - logf(z) : -kInf;
+        lps[i] = in ? 2.f * (half_diff(KeyTraits<Raw>::decode(static_cast<uint32_t>(e >> 32)), vmax) / t) - logf(z)
+                    : -kInf;
     }
     if (tid == 0 && P.status) P.status[row] = 0u;
   }

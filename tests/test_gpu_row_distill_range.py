@@ -160,3 +160,18 @@ def test_small_temperatures(dtype, tail, t, vocab):
     x[1, out] = 14.0
     x[2, int(ids[2, 0])] = x[2, next(j for j in range(700, vocab) if j not in ids[2].tolist())] = 14.0
     check(x, ids.cuda(), lp.cuda(), t, tail, vocab)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("tail", [False, True])
+@pytest.mark.parametrize("vocab", [1003, 20_011, 1 << 20])
+def test_differences_beyond_fp32(dtype, tail, vocab):
+    """Logits at both ends of the type: their difference overflows fp32, their
+    difference over T does not."""
+    g = torch.Generator().manual_seed(9)
+    x = ((torch.rand((3, vocab + (-vocab) % 8), generator=g) * 2 - 1) * 3.0e38).to(dtype).cuda()
+    x[1, :vocab] = -3.0e38
+    x[1, 5] = 3.0e38
+    x[2, :vocab:2] = 3.0e38
+    ids, lp = listed(3, vocab, 30, seed=36)
+    check(x, ids.cuda(), lp.cuda(), 1e38, tail, vocab, g=1e30)

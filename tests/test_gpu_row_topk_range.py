@@ -53,3 +53,15 @@ def test_common_offsets(vocab, offset):
 @pytest.mark.parametrize("t", [1e-2, 1e-3, 1e-6, 1e-9, 1e-12])
 def test_small_temperatures(dtype, vocab, t):
     check(logits_on("cuda", 3, vocab, dtype, seed=6), 60, vocab, t)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("vocab", [1003, 20_011, 1 << 20])
+def test_differences_beyond_fp32(dtype, vocab):
+    """Logits at both ends of the type: their difference overflows fp32, their
+    difference over T does not."""
+    g = torch.Generator().manual_seed(9)
+    x = ((torch.rand((3, vocab + (-vocab) % 8), generator=g) * 2 - 1) * 3.0e38).to(dtype).cuda()
+    x[1, :vocab] = -3.0e38
+    x[1, 5] = 3.0e38
+    check(x, 60, vocab, 1e38)
