@@ -42,10 +42,12 @@ struct alignas(16) DistillCtx {
   float ref, lz;    // of the dense part: the whole row's, or what lies outside the list
   float coef;       // factor of the dense part: 1, or q_t - a_t
   float rall, lall; // the whole row's
-  float tnorm;      // teacher: a_k = exp(lp_k - tnorm)
+  // teacher: a_k = exp((lp_k - tref) - tlog).  In list mode tref is the list's largest value, so that values
+  // of any size keep their differences (one sum of both would round them away)
+  float tref, tlog;
   uint32_t zero;    // no gradient (empty list, non-finite row)
   uint32_t dup;     // the list repeats an id
-  uint32_t pad[6];
+  uint32_t pad[5];
 };
 static_assert(sizeof(DistillCtx) == VS_CTX_BYTES_PER_ROW, "ctx layout");
 
@@ -117,7 +119,7 @@ __device__ __forceinline__ void grad_pass(const Raw* __restrict__ row, G* __rest
     const int id = s < width ? ids[s] : -1;
     if (id >= j0 && id < j1 && (!k.dup || first_of(ids, s))) {
       const float q = ex2(fmaf(half_diff(value_of(row[id]), k.rall), c2, -k.lall));
-      float d = scale * (q - expf(lp[s] - k.tnorm));
+      float d = scale * (q - expf(lp[s] - k.tref - k.tlog));
       if constexpr (ACC) d += old[i];
       out[id] = to_grad<G>(d);
     }
@@ -327,7 +329,7 @@ __global__ void __launch_bounds__(kDThreads) distill_fwd_kernel(DistillParams P)
   const double at = tail ? fmax(0.0, 1.0 - sum.a) : 0.0;
   const double qt = zr > 0.0 ? exp2(lr) : 0.0;
   const bool empty = any == 0u || (!tail && !(sum.a > 0.0));
-  const double tnorm = tail ? 0.0 : toff + log(sum.a);
+  const double tlog = tail ? 0.0 : log(sum.a);
   const bool live = fine && !bad && !empty;
 
   constexpr double kLn2d = 0.69314718055994530942;
@@ -335,7 +337,7 @@ __global__ void __launch_bounds__(kDThreads) distill_fwd_kernel(DistillParams P)
 #pragma unroll
   for (int i = 0; i < SLOTS; ++i)
     if (kept[i] && live) {
-      const double l = lp[i] - tnorm, a = exp(l);
+      const double l = lp[i] - toff - tlog, a = exp(l);
       if (a > 0.0) loss += a * (l - kLn2d * ((u[i] - m) * cd - lz));
     }
   Three fin = block_three<false>(Three{loss, 0.0, 0.0}, sh.red);
@@ -351,7 +353,8 @@ __global__ void __launch_bounds__(kDThreads) distill_fwd_kernel(DistillParams P)
   k.ref = outside ? static_cast<float>(mr) : k.rall;
   k.lz = outside ? static_cast<float>(log2(zr)) : k.lall;
   k.coef = tail ? (outside ? static_cast<float>(qt - at) : 0.f) : 1.f;
-  k.tnorm = static_cast<float>(tnorm);
+  k.tref = static_cast<float>(toff);
+  k.tlog = static_cast<float>(tlog);
   k.zero = live ? 0u : 1u;
   k.dup = sh.dup;
   if (rank == 0 && tid == 0) {
@@ -433,7 +436,8 @@ struct alignas(16) DistillStage {
   DistillPart parts[kSMaxCluster];  // from the CTA of each rank
   DistillCtx k;
   uint64_t bar, xbar;  // the slice's copy; the parts
-  double s0, t1, tnorm, at;
+  double s0, t1, tlog, at;
+  float tref;
   float red_m[kSWarps];
   double red_z[kSWarps];
   uint32_t status, dup, any, bad;
@@ -553,8 +557,8 @@ __global__ void __launch_bounds__(kSThreads, 5) distill_stage_kernel(DistillPara
   DistillPart mine{-kInf, -kInf, 0.0, 0.0, 0.0, 0.0, 0u, 0u};
   const double cd = static_cast<double>(c);  // the same factor everywhere: its rounding cancels
   if (tid < 32) {
-    // the list: the teacher's sums s0 = sum w, t1 = sum w lp with w = exp(lp - off) over all of it, and the
-    // student's over this slice's elements
+    // the list: the teacher's sums s0 = sum w, t1 = sum w (lp - off) with w = exp(lp - off) over all of it, and
+    // the student's over this slice's elements
     float off = -kInf;
     if (!tail)
       for (int s = lane; s < W; s += 32)
@@ -578,7 +582,7 @@ __global__ void __launch_bounds__(kSThreads, 5) distill_stage_kernel(DistillPara
         const double below = static_cast<double>(l) - static_cast<double>(off), x2 = below * 1.4426950408889634;
         const double w = fabs(x2) <= 1000.0 ? exp2_near(x2) : exp(below);
         s0 += w;
-        t1 += w * static_cast<double>(l);
+        t1 += w * below;
         if (own && w > 0.0) {
           ws += w;
           if (lmax > -kInf) wu += w * ((static_cast<double>(u) - static_cast<double>(lmax)) * cd);
@@ -596,7 +600,8 @@ __global__ void __launch_bounds__(kSThreads, 5) distill_stage_kernel(DistillPara
     if (lane == 0) {
       sh.s0 = s0;
       sh.t1 = t1;
-      sh.tnorm = tail ? 0.0 : static_cast<double>(off) + log(s0);
+      sh.tref = off;
+      sh.tlog = tail ? 0.0 : log(s0);
       sh.at = tail ? fmax(0.0, 1.0 - s0) : 0.0;
     }
   } else {
@@ -649,7 +654,8 @@ __global__ void __launch_bounds__(kSThreads, 5) distill_stage_kernel(DistillPara
       k.ref = outside ? a : b;
       k.lz = outside ? log2f(za) : k.lall;
       k.coef = tail ? (outside ? static_cast<float>(static_cast<double>(exp2f(half_diff(a, b) * c2) * za / zb) - sh.at) : 0.f) : 1.f;
-      k.tnorm = static_cast<float>(sh.tnorm);
+      k.tref = sh.tref;
+      k.tlog = static_cast<float>(sh.tlog);
       k.zero = live ? 0u : 1u;
       k.dup = sh.dup;
       sh.k = k;
@@ -665,7 +671,7 @@ __global__ void __launch_bounds__(kSThreads, 5) distill_stage_kernel(DistillPara
       const double lz = log2(zld + (zad > 0.0 ? zad * exp2_below((ad - bd) * cd) : 0.0));
       constexpr double kLn2d = 0.69314718055994530942;
       const double norm = tail ? 1.0 : 1.0 / sh.s0;  // a = w * norm
-      double loss = (sh.t1 - sh.s0 * sh.tnorm + kLn2d * (lz * sh.s0 - su)) * norm;
+      double loss = (sh.t1 - sh.s0 * sh.tlog + kLn2d * (lz * sh.s0 - su)) * norm;
       if (tail && sh.at > 0.0 && zad > 0.0) {
         const double lq = (ad - bd) * cd + log2(zad) - lz;
         loss += sh.at * (log(sh.at) - kLn2d * lq);
@@ -727,7 +733,7 @@ __global__ void __launch_bounds__(kSThreads, 5) distill_stage_kernel(DistillPara
       for (int s = tid; s < W; s += kSThreads) {
         const int id = ids[s];
         if (id >= j0 && id < j1)
-          out[id] = to_grad<G>(scale * (ex2(fmaf(half_diff(us[s], k.rall), 2.f * k.c, -k.lall)) - expf(lps[s] - k.tnorm)));
+          out[id] = to_grad<G>(scale * (ex2(fmaf(half_diff(us[s], k.rall), 2.f * k.c, -k.lall)) - expf(lps[s] - k.tref - k.tlog)));
       }
   }
 }

@@ -51,7 +51,7 @@ def plain_row(x, ids, lp, t, tail):
     z = z - z.max()
     logq = z - log_sum(z)
     lp = lp.astype(np.float64)
-    la = lp if tail else lp - log_sum(lp)
+    la = lp if tail else lp - lp.max() - log_sum(lp - lp.max())
     a = np.exp(la)
     loss = float((a * (la - logq[ids])).sum())
     full = np.zeros(len(x))
@@ -175,3 +175,13 @@ def test_differences_beyond_fp32(dtype, tail, vocab):
     x[2, :vocab:2] = 3.0e38
     ids, lp = listed(3, vocab, 30, seed=36)
     check(x, ids.cuda(), lp.cuda(), 1e38, tail, vocab, g=1e30)
+
+
+@pytest.mark.parametrize("offset", [30.0, -1e3, 1e4, 1e6, -1e9, 1e30])
+@pytest.mark.parametrize("vocab", [1003, 1 << 20])
+def test_teacher_logits_of_any_size(offset, vocab):
+    """List mode takes any logits: a common offset (and what it rounds away
+    from the values, which the plain form sees too) changes nothing."""
+    x = logits_on("cuda", 3, vocab, F32, seed=10)
+    ids, lp = listed(3, vocab, 30, seed=37)
+    check(x, ids.cuda(), (lp + offset).cuda(), 1.0, False, vocab)
