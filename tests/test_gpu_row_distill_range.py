@@ -185,3 +185,18 @@ def test_teacher_logits_of_any_size(offset, vocab):
     x = logits_on("cuda", 3, vocab, F32, seed=10)
     ids, lp = listed(3, vocab, 30, seed=37)
     check(x, ids.cuda(), (lp + offset).cuda(), 1.0, False, vocab)
+
+
+@pytest.mark.parametrize("vocab", [1003, 20_011])
+def test_a_list_with_almost_all_of_the_mass(vocab):
+    """The list leaves 1e-6, the student almost nothing: outside the list the
+    gradient is -a_t r_j, so a_t = 1 - sum a has to hold to 2e-5 of itself,
+    2e-11 of the sum.  The shares lie half way between powers of two, where a
+    polynomial in the exponent's fraction is at its worst."""
+    share = [2.0 ** -0.5, 2.0 ** -2.5, 2.0 ** -3.5]
+    share.append(1 - 1e-6 - sum(share))
+    lp = torch.log(torch.tensor([share, share[::-1]], dtype=torch.float64)).float()
+    ids = torch.tensor([[3, 501, 77, 1002], [7, 9, 1000, 6]], dtype=torch.int32)
+    x = logits_on("cpu", 2, vocab, F32, seed=11, sigma=1.0, spikes=0)
+    x.scatter_(1, ids.long(), lp + 30.0)
+    check(x.cuda(), ids.cuda(), lp.cuda(), 1.0, True, vocab)
