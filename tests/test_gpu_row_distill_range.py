@@ -200,3 +200,35 @@ def test_a_list_with_almost_all_of_the_mass(vocab):
     x = logits_on("cpu", 2, vocab, F32, seed=11, sigma=1.0, spikes=0)
     x.scatter_(1, ids.long(), lp + 30.0)
     check(x.cuda(), ids.cuda(), lp.cuda(), 1.0, True, vocab)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("vocab", [1003, 20_011, 151_936])
+def test_a_loss_near_zero(dtype, vocab):
+    """A teacher close to its student.  The loss is a difference of logarithms
+    of about its square in size, so it is taken in fp64, and the fp32 parts
+    enter by derivatives that vanish with it: the share outside the list (off by
+    e <= 5e-6: 2^-22 for the exponential, 2^-24 of an argument of at most 60,
+    2^-24 for each of at most 24 additions, 2^-22 and 2^-23 * 30 for a thread's
+    reference) by (q_t - a_t) e, the factor 1 / T (2^-23) by the difference of
+    the means of z under q and under a.  The result is rounded once; 1e-11 for
+    the squares and for fp64."""
+    rows, k = 6, 64
+    x = logits_on("cuda", rows, vocab, dtype, seed=12)
+    g = torch.Generator().manual_seed(38)
+    xs = x[:, :vocab].double().cpu()
+    y = xs + 0.03 * torch.randn(xs.shape, generator=g, dtype=torch.float64)
+    v, ids = torch.topk(y, k, dim=1)
+    lp = (v - torch.logsumexp(y, 1, keepdim=True)).float()
+    out = vsb.distill_fwd(x, ids.to(torch.int32).cuda(), lp.cuda(), tail=True, vocab=vocab)
+    for r in range(rows):
+        li, ll = ids[r].numpy(), lp[r].numpy()
+        z = xs[r].numpy()
+        want, _, _, q, a = plain_row(z, li, ll, 1.0, True)
+        off = np.ones(vocab, bool)
+        off[li] = False
+        qt, at = q[off].sum(), 1 - a.sum()
+        mean = ((q[li] - a[li]) * z[li]).sum() + (qt - at) * (q[off] * z[off]).sum() / qt
+        tol = 5e-6 * abs(qt - at) + 2.0 ** -23 * abs(mean) + 2.0 ** -24 * want + 1e-11
+        assert want < 2e-3 and tol < 2e-7
+        assert abs(float(out["loss"][r]) - want) <= tol, (r, float(out["loss"][r]), want, tol)
