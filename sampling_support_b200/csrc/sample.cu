@@ -54,7 +54,7 @@ __device__ __noinline__ void draw_from_list(const SampleParams& P, int row, cons
     u64 m = 0ull;
     for (uint32_t i = lane; i < n; i += 32) {
       const float v = KeyTraits<Raw>::decode(static_cast<uint32_t>(sh.sorted[i] >> 32));
-      if (M.w(v) >= static_cast<double>(s.m)) {
+      if (M.reaches(v, s.m)) {
         ++keep;
         m += sh.list[i];
       }
@@ -71,7 +71,7 @@ __device__ __noinline__ void draw_from_list(const SampleParams& P, int row, cons
   }
 }
 
-// The smallest key in [lo, hi] whose mass is at least m (w(hi) >= m): the
+// The smallest key in [lo, hi] that reaches min-p's m (hi does): the
 // lanes of one warp test 32 keys at a time.
 template <typename Raw>
 __device__ __forceinline__ uint32_t first_above(const RsMass& M, float m, uint32_t lo, uint32_t hi) {
@@ -79,7 +79,7 @@ __device__ __forceinline__ uint32_t first_above(const RsMass& M, float m, uint32
   while (lo < hi) {
     const uint32_t step = (hi - lo) / 32u + 1u;
     const uint32_t off = min(hi - lo, lane * step);
-    const uint32_t yes = __ballot_sync(0xffffffffu, M.w(KeyTraits<Raw>::decode(lo + off)) >= static_cast<double>(m));
+    const uint32_t yes = __ballot_sync(0xffffffffu, M.reaches(KeyTraits<Raw>::decode(lo + off), m));
     const int l = yes ? __ffs(yes) - 1 : 32;  // hi itself passes
     const uint32_t top = l == 32 ? hi : lo + min(hi - lo, l * step);
     lo = l == 0 ? lo : lo + min(hi - lo, (l - 1) * step) + 1u;
@@ -187,7 +187,7 @@ __device__ __noinline__ void draw_step(RsMsg* out) {
           kb_keys<Raw>(b, klo, khi);
           klo = min(klo, ktop);
           khi = min(khi, ktop);
-          if (!(M.w(KeyTraits<Raw>::decode(klo)) >= static_cast<double>(s.m))) break;
+          if (!M.reaches(KeyTraits<Raw>::decode(klo), s.m)) break;
         }
         if (b == kKbBins) continue;
         const int at = (b & ~31) + lane;
@@ -198,7 +198,7 @@ __device__ __noinline__ void draw_step(RsMsg* out) {
         f.mass = sh.run_mass[b >> 5] + rs_warp_sum(at < b ? m : 0ull);
         f.n = __shfl_sync(0xffffffffu, c, b & 31);
         if (f.cnt >= n) continue;
-        if (f.n == 0ull || !(M.w(KeyTraits<Raw>::decode(khi)) >= static_cast<double>(s.m))) {
+        if (f.n == 0ull || !M.reaches(KeyTraits<Raw>::decode(khi), s.m)) {
           n = f.cnt;
           mass = f.mass;
           continue;
@@ -375,7 +375,7 @@ static __device__ __noinline__ bool draw_by_counts(bool middle) {
       uint32_t klo, khi;
       kb_keys<uint16_t>(b, klo, khi);
       if (b == static_cast<int>(kKbSpan)) khi = 0x7FFFu;
-      if (b > b0 && !(M.w(KeyTraits<uint16_t>::decode(khi)) >= static_cast<double>(s.m))) break;
+      if (b > b0 && !M.reaches(KeyTraits<uint16_t>::decode(khi), s.m)) break;
     }
     if (b < kKbBins) {
       if (middle && (b == static_cast<int>(kKbSpan) || b == static_cast<int>(kKbSpan) + 1)) return false;
@@ -438,8 +438,8 @@ __device__ __forceinline__ bool draw_by_value(const SampleParams& P, int row, co
         cta_sync();
         if (!kb_chunks<uint16_t, true>())
           flag = 2u;  // every token masked
-        else if (low && sh.M.z(-131072.f) >= -46.0)
-          flag = 1u;  // the last bin's values have masses of their own
+        else if (low && (sh.M.z(-131072.f) >= -46.0 || (s.m > 0.f && sh.M.reaches(-131072.f, s.m))))
+          flag = 1u;  // the last bin's values have masses of their own, or min-p may tell them apart
       }
       if (threadIdx.x >= 32) return;
       if (flag == 0u && !draw_by_counts(middle)) flag = 3u;
