@@ -126,8 +126,9 @@ __host__ __device__ inline int sample_list_k(int vocab, float t, int top_k) {
   return top_k > 0 && top_k < vocab && top_k <= kListTopK ? top_k : 0;
 }
 #ifdef __CUDACC__
-// The running mass that a row's number asks for: the first integer above
-// u * mass, at most the mass itself (u = 1 takes the last token).
+// The running mass that a row's number below 1 asks for: the first integer above
+// u * mass.  The number 1 asks for the support's last token by its place, as
+// masses at the support's end may round to nothing.
 __device__ __forceinline__ unsigned long long draw_target(float u, unsigned long long mass) {
   const double x = floor(static_cast<double>(u) * static_cast<double>(mass));
   const unsigned long long t = x >= static_cast<double>(mass) ? mass : static_cast<unsigned long long>(x) + 1ull;

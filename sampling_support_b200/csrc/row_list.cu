@@ -330,7 +330,8 @@ struct SampleOp {
       cross(n, ~0ull, mass);
     }
     u64 upto;
-    const uint32_t at = cross(n, draw_target(P.uniform[row], mass), upto);
+    const float u = P.uniform[row];
+    const uint32_t at = u < 1.f ? cross(n, draw_target(u, mass), upto) : n - 1u;
     if (lane == 0) {
       P.token[row] = static_cast<int32_t>(~static_cast<uint32_t>(sorted[at]));
       if (P.logprob) P.logprob[row] = static_cast<float>(z_of(at) - log(static_cast<double>(mass) / scale));

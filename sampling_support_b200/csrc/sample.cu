@@ -5,7 +5,7 @@
 //   n_k = top_k, n_p = the first i with C_i >= top_p C_{n_k},
 //   n_m = the number of tokens with w >= min_p;  the support is the first
 //   n = min(n_k, n_p, n_m) tokens;
-//   token = the first i with C_i > u C_n,  logprob = log(w_i / C_n).
+//   token = the first i with C_i > u C_n (u = 1: the n-th),  logprob = log(w_i / C_n).
 #include "internal.h"
 #include "row_select.cuh"
 #include "row_stage.cuh"
@@ -63,7 +63,7 @@ __device__ __noinline__ void draw_from_list(const SampleParams& P, int row, cons
     mass = rs_warp_sum(m);
   }
   u64 upto = 0ull;
-  const uint32_t at = rs_list_cross(sh, n, draw_target(s.u, mass), upto);
+  const uint32_t at = s.u < 1.f ? rs_list_cross(sh, n, draw_target(s.u, mass), upto) : n - 1u;
   if (lane == 0) {
     const u64 e = sh.sorted[at];
     P.token[row] = static_cast<int32_t>(~static_cast<uint32_t>(e));
@@ -208,8 +208,8 @@ __device__ __noinline__ void draw_step(RsMsg* out) {
         q.khi = khi;
         break;
       } else {
-        by_mass = true;
-        t = draw_target(s.u, mass);
+        by_mass = s.u < 1.f;
+        t = by_mass ? draw_target(s.u, mass) : n;
       }
       f = kb_find<false>(by_mass, t);
       if (phase == 1 && f.cnt >= n) {  // not before the top-k cut
@@ -388,14 +388,15 @@ static __device__ __noinline__ bool draw_by_counts(bool middle) {
       }
     }
   }
-  const u64 t = draw_target(s.u, mass);
-  const RsBin f = kb_find<true>(true, t);
+  const bool by_mass = s.u < 1.f;
+  const u64 t = by_mass ? draw_target(s.u, mass) : n;
+  const RsBin f = kb_find<true>(by_mass, t);
   if (lost(f)) return false;
   if (lane == 0) {
     uint32_t klo, khi;
     kb_keys<uint16_t>(f.bin, klo, khi);
     d.key = f.bin == static_cast<int>(kKbSpan) ? 0x7FFFu : khi;
-    d.t = place_in_group(t - f.mass, sh.w[f.bin]);
+    d.t = by_mass ? place_in_group(t - f.mass, sh.w[f.bin]) : t - f.cnt;
     d.n = n;
     d.mass = mass;
   }
@@ -438,8 +439,8 @@ __device__ __forceinline__ bool draw_by_value(const SampleParams& P, int row, co
         cta_sync();
         if (!kb_chunks<uint16_t, true>())
           flag = 2u;  // every token masked
-        else if (low && (sh.M.z(-131072.f) >= -46.0 || (s.m > 0.f && sh.M.reaches(-131072.f, s.m))))
-          flag = 1u;  // the last bin's values have masses of their own, or min-p may tell them apart
+        else if (low && (s.u >= 1.f || sh.M.z(-131072.f) >= -46.0 || (s.m > 0.f && sh.M.reaches(-131072.f, s.m))))
+          flag = 1u;  // the last bin's values have masses of their own, or min-p or the draw may tell them apart
       }
       if (threadIdx.x >= 32) return;
       if (flag == 0u && !draw_by_counts(middle)) flag = 3u;

@@ -1,4 +1,5 @@
-"""vs_sample over the whole range of its settings: min-p of any size."""
+"""vs_sample over the whole range of its settings: min-p of any size,
+and the uniform number 1."""
 
 import pytest
 import torch
@@ -50,13 +51,31 @@ def test_smallest_min_p(dtype, min_p, top_k):
 @pytest.mark.parametrize("dtype", [BF, F32])
 @pytest.mark.parametrize("min_p", [0.0, 1e-22, 1e-30, 1e-40])
 def test_far_negative_logits(dtype, min_p):
-    """Values below -2^17 that min-p tells apart."""
+    """Values below -2^17 that min-p tells apart, and the last of them drawn."""
     vocab = 3001
     x = torch.full((4, 3008), float("nan"), device="cuda")
     x[:, :vocab] = torch.linspace(0.0, -3.0e5, vocab).cuda()
     x[1, :vocab] = x[1, :vocab].flip(0)
     x[2, 100:vocab] = -1.5e5
     x[3, 200:vocab] = float("-inf")
-    u = torch.tensor([0.3, 0.9, 0.99, 0.6]).cuda()
+    u = torch.tensor([0.3, 1.0, 1.0, 1.0]).cuda()
     for t in (2500.0, 1.0, 1e5):
         check_both(x.to(dtype), u, vocab, t=t, m=min_p)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("vocab", [1003, 5003, 50_021])
+@pytest.mark.parametrize("kw", [{}, dict(k=300), dict(k=900), dict(p=0.9), dict(k=500, p=0.9999), dict(m=1e-9),
+                                dict(m=1e-30), dict(k=900, m=1e-30)], ids=str)
+def test_the_number_one_takes_the_last_token(dtype, vocab, kw):
+    """u = 1 is the support's last token also where the masses at its end round
+    to nothing: values spread over 300 nats, a crowd of equal values at the
+    end, masked tokens behind, zeros and values next to them."""
+    x = logits_on("cuda", 5, vocab, dtype, seed=22)
+    x[1, vocab // 2:vocab] = -60.0
+    x[2, 64:vocab] = float("-inf")
+    x[3, :vocab:3] = 0.0
+    x[3, 1:vocab:3] = 2.0 ** -40
+    x[4, :vocab] = x[4, :vocab] * 20
+    u = torch.tensor([1.0, 1.0, 1.0, 1.0, 1.0]).cuda()
+    check_both(x, u, vocab, t=0.25, **kw)
