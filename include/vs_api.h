@@ -480,8 +480,11 @@ typedef struct vs_sample_args {
  *   n_m = number of tokens with w >= min_p, n = min(n_k, n_p, n_m);
  *   token[r] = the first i <= n with C_i > u C_n (u = 1: the n-th),
  *   logprob[r] = log(w_token / C_n), support_size[r] = n.
- * Sums are exact (fixed point, w in fp64), so equal inputs give equal tokens
- * on every call and every batch.  A logit of -inf is a masked token: it is in
+ * Masses are w in fp64 rounded to fixed point (2^-45 of the largest for
+ * 151,936 tokens, 2^-43 for VS_MAX_ROW_VOCAB; bf16 logits within 2^-24 of zero
+ * may count as zeros where that moves the row's sum by less than 2^-40), and
+ * their sums do not depend on the order: a row gets the same token on every call
+ * and in every batch.  A logit of -inf is a masked token: it is in
  * no set, whatever the filters.  Rows without a token get -1, NaN and 0: every
  * token masked (VS_ROW_EMPTY_SUPPORT), a NaN or +inf logit
  * (VS_ROW_NONFINITE_INPUT), or a setting outside its range: T negative or not

@@ -289,12 +289,10 @@ struct SampleOp {
       p = 1.f;
       m = 0.f;
     }
-    const double inv_t = 1.0 / static_cast<double>(t), scale = static_cast<double>(1ull << P.fx_shift);
-    auto z_of = [&](uint32_t i) {
-      const float v = KeyTraits<Raw>::decode(static_cast<uint32_t>(sorted[i] >> 32));
-      return (static_cast<double>(v) - static_cast<double>(vmax)) * inv_t;
-    };
-    for (uint32_t i = threadIdx.x; i < nk; i += kLThreads) masses[i] = __double2ull_rn(exp(z_of(i)) * scale);
+    RowMass M;
+    M.set(vmax, t, P.fx_shift);
+    auto value = [&](uint32_t i) { return KeyTraits<Raw>::decode(static_cast<uint32_t>(sorted[i] >> 32)); };
+    for (uint32_t i = threadIdx.x; i < nk; i += kLThreads) masses[i] = M.fixed(value(i), [](int j) { return exp2_64th(j); });
     cta_sync();
     if (threadIdx.x >= 32) return;
     const int lane = threadIdx.x;
@@ -325,7 +323,7 @@ struct SampleOp {
     if (p < 1.f) n = cross(nk, topp_target(p, static_cast<double>(mass)), mass) + 1u;
     if (m > 0.f) {
       uint32_t keep = 0u;  // the order is by mass: those kept are the first ones
-      for (uint32_t i = lane; i < n; i += 32) keep += exp(z_of(i)) >= static_cast<double>(m) ? 1u : 0u;
+      for (uint32_t i = lane; i < n; i += 32) keep += M.reaches(value(i), m) ? 1u : 0u;
       n = __reduce_add_sync(0xffffffffu, keep);
       cross(n, ~0ull, mass);
     }
@@ -334,7 +332,7 @@ struct SampleOp {
     const uint32_t at = u < 1.f ? cross(n, draw_target(u, mass), upto) : n - 1u;
     if (lane == 0) {
       P.token[row] = static_cast<int32_t>(~static_cast<uint32_t>(sorted[at]));
-      if (P.logprob) P.logprob[row] = static_cast<float>(z_of(at) - log(static_cast<double>(mass) / scale));
+      if (P.logprob) P.logprob[row] = M.logprob(value(at), mass);
       if (P.support_size) P.support_size[row] = static_cast<int32_t>(n);
       if (P.status) P.status[row] = 0u;
     }

@@ -5,9 +5,12 @@
 // -inf is a masked token and belongs to no set.  A selection asks for the
 // element at which a running count, or a running sum of masses
 // w_j = exp((l_j - max l) / T), first reaches a target.  Masses are 64-bit
-// fixed point, w * 2^fx with vocab * 2^fx <= 2^62, each w computed in fp64:
-// every sum is exact whatever its order, and the decisions are those of the
-// formula in 64 bits to about 2^-45 of the row's largest mass.
+// fixed point (RowMass), vocab * 2^fx <= 2^62: their sums are exact whatever
+// the order, so every path of the kernels takes the same decisions.  Each mass is
+// off by at most 2^-(fx+1) of the row's largest, a sum of n by n of these (2^-28
+// for a full row of 151,936) and by 4e-14 of itself.  (A bf16 row that is drawn
+// from by its values may count those within 2^-24 of zero as zeros, where that
+// moves its sum by less than 2^-40.)
 //
 // The row is split into one contiguous slice per CTA of the cluster.  Every
 // pass re-reads the slice (the first one from HBM, the others from L2, where a
@@ -57,39 +60,10 @@ struct RsMsg {
 
 __device__ __forceinline__ const double* rs_tab();  // 2^(i/64), shared
 
-// A call of its own: in line at its six places the kernels spill more (64.5 against 63.3 us for 64 x 151,936 fp32).
-static __device__ __noinline__ bool rs_reaches(double z, float m) { return exp(z) >= static_cast<double>(m); }
-
-// The masses of one row: w(v) = exp((v - vmax) / T) and its fixed-point value.
-// exp(z) = 2^(k/64) 2^(f/64), k = rint(64 z log2 e), |f| <= 1/2: a 64-entry
-// table of 2^(i/64) and the Taylor polynomial of degree 4 in f ln2 / 64
-// (remainder below 4e-14), the table-driven method of Tang (1989).  Ten fp64
-// operations: 3.7 elements per clock and SM against 2.3 for exp().
-struct RsMass {
-  double vmax;   // largest logit
-  double inv_t;  // 1 / T
-  double scale;  // 2^fx
-  double c64;    // 64 log2(e) / T
-  int fx;
-
-  __device__ __forceinline__ double z(float v) const { return (static_cast<double>(v) - vmax) * inv_t; }
-  // w * 2^up for z >= -46 nats (up <= 50), 0 below (there w < 2^-66)
-  __device__ __forceinline__ double scaled(float v, int up) const {
-    constexpr double kA = 0.010830424696249145;  // ln 2 / 64
-    const double x = (static_cast<double>(v) - vmax) * c64;
-    const double r = x + 6755399441055744.0;  // 1.5 * 2^52: the integer lands in the low word
-    const int k = __double2loint(r);
-    const double f = x - (r - 6755399441055744.0);
-    double p = fma(fma(fma(fma(f, kA * kA * kA * kA / 24.0, kA * kA * kA / 6.0), f, kA * kA / 2.0), f, kA), f, 1.0);
-    p *= rs_tab()[k & 63];
-    const double w = __hiloint2double(__double2hiint(p) + (((k >> 6) + up) << 20), __double2loint(p));
-    return x >= -4247.0 ? w : 0.0;  // 46 nats in units of ln 2 / 64
-  }
-  // min-p's test, w >= m: on the exponential itself, which is not cut at 46 nats (m may be smaller)
-  __device__ __forceinline__ bool reaches(float v, float m) const { return rs_reaches(z(v), m); }
+// The masses of one row, with the table in shared memory.
+struct RsMass : RowMass {
   __device__ __forceinline__ u64 fixed(float v) const {
-    // w 2^fx <= 2^50: adding 2^52 rounds it to an integer in the mantissa
-    return static_cast<u64>(__double_as_longlong(scaled(v, fx) + 4503599627370496.0)) & 0xFFFFFFFFFFFFFull;
+    return RowMass::fixed(v, [](int i) { return rs_tab()[i]; });
   }
 };
 
@@ -176,11 +150,8 @@ __device__ __forceinline__ const double* rs_tab() { return rs_shared().tab; }
 // after the block's next barrier.
 __device__ __forceinline__ void rs_set_masses(float v, float t, int shift) {
   RsShared& sh = rs_shared();
-  if (threadIdx.x < 64) sh.tab[threadIdx.x] = exp2(static_cast<double>(threadIdx.x) * (1.0 / 64.0));
-  if (threadIdx.x == 64) {
-    const double inv_t = 1.0 / static_cast<double>(t);
-    sh.M = RsMass{static_cast<double>(v), inv_t, static_cast<double>(1ull << shift), 92.332482616893656 * inv_t /* 64 / ln 2 */, shift};
-  }
+  if (threadIdx.x < 64) sh.tab[threadIdx.x] = exp2_64th(threadIdx.x);
+  if (threadIdx.x == 64) sh.M.set(v, t, shift);
 }
 
 // The slice of one row that this CTA holds, and the cluster around it.

@@ -21,9 +21,8 @@ __device__ __forceinline__ void write_none(const SampleParams& P, int row, uint3
   if (P.status) P.status[row] = status;
 }
 
-__device__ __forceinline__ void write_row(const SampleParams& P, int row, double z, u64 mass, u64 n,
-                                          const RsMass& M) {
-  if (P.logprob) P.logprob[row] = static_cast<float>(z - log(static_cast<double>(mass) / M.scale));
+__device__ __forceinline__ void write_row(const SampleParams& P, int row, float v, u64 mass, u64 n, const RsMass& M) {
+  if (P.logprob) P.logprob[row] = M.logprob(v, mass);
   if (P.support_size) P.support_size[row] = static_cast<int32_t>(n);
   if (P.status) P.status[row] = 0u;
 }
@@ -67,7 +66,7 @@ __device__ __noinline__ void draw_from_list(const SampleParams& P, int row, cons
   if (lane == 0) {
     const u64 e = sh.sorted[at];
     P.token[row] = static_cast<int32_t>(~static_cast<uint32_t>(e));
-    write_row(P, row, M.z(KeyTraits<Raw>::decode(static_cast<uint32_t>(e >> 32))), mass, n, M);
+    write_row(P, row, KeyTraits<Raw>::decode(static_cast<uint32_t>(e >> 32)), mass, n, M);
   }
 }
 
@@ -314,7 +313,7 @@ __device__ __forceinline__ void draw_from_bins(const SampleParams& P, int row, c
     if (R.rank == 0 && threadIdx.x == 0) {
       const RsDraw& d = sh.draw;
       if (msg.op == kRsStop) P.token[row] = d.id;
-      write_row(P, row, sh.M.z(KeyTraits<Raw>::decode(d.key)), d.mass, d.n, sh.M);
+      write_row(P, row, KeyTraits<Raw>::decode(d.key), d.mass, d.n, sh.M);
     }
     __syncwarp();
     if (msg.op == kRsTies) draw_tie<Raw>(msg.klo, msg.a, P.token + row);
@@ -408,8 +407,10 @@ static __device__ __noinline__ bool draw_by_counts(bool middle) {
 // atomic per element and no exponential), the decisions by the leader, and a
 // second pass from L2 that finds the drawn token among those of its value.
 // Returns false when the row needs the general path: values beyond the bins'
-// range that matter.
-__device__ __forceinline__ bool draw_by_value(const SampleParams& P, int row, const Settings& s, RsRow<uint16_t>& R) {
+// range that matter.  `exact`: values next to zero matter too, so that a row
+// whose list overflowed gets the list kernel's answer to the last unit.
+__device__ __forceinline__ bool draw_by_value(const SampleParams& P, int row, const Settings& s, RsRow<uint16_t>& R,
+                                              bool exact) {
   RsShared& sh = rs_shared();
   rs_set_masses(0.f, s.t, P.fx_shift);  // the maximum follows
   if (threadIdx.x == 0) sh.draw.s = s;
@@ -432,6 +433,10 @@ __device__ __forceinline__ bool draw_by_value(const SampleParams& P, int row, co
     __syncwarp();
   }
   bool chunks = false, middle = ends.klo != 0u;
+  if (middle && exact) {
+    if (kb_tiny()) return false;
+    middle = false;
+  }
   for (;;) {
     const RsMsg got = R.broadcast([&](RsMsg* msg) {
       uint32_t flag = 0u;
@@ -462,7 +467,7 @@ __device__ __forceinline__ bool draw_by_value(const SampleParams& P, int row, co
       if (got.flag == 2u)
         write_none(P, row, VS_ROW_EMPTY_SUPPORT);
       else
-        write_row(P, row, sh.M.z(KeyTraits<uint16_t>::decode(got.key)), sh.draw.mass, sh.draw.n, sh.M);
+        write_row(P, row, KeyTraits<uint16_t>::decode(got.key), sh.draw.mass, sh.draw.n, sh.M);
     }
     __syncwarp();
     if (got.flag == 0u) draw_tie<uint16_t>(got.key, got.a, P.token + row);
@@ -491,10 +496,10 @@ __device__ __forceinline__ void sample_row(const SampleParams& P, int row) {
     s.m = 0.f;
   }
   bool by_list = !P.lists && sample_list_k(P.vocab, s.t, s.k) > 0;
-  bool by_value = sizeof(Raw) == 2 && fine && !by_list;
+  bool by_value = sizeof(Raw) == 2 && fine && !by_list, crowd = false;
   for (;;) {
     if constexpr (sizeof(Raw) == 2) {
-      if (by_value && draw_by_value(P, row, s, R)) return;
+      if (by_value && draw_by_value(P, row, s, R, crowd)) return;
     }
     cta_sync();  // the geometry
     const uint32_t kmax = rs_max<Raw>();
@@ -517,6 +522,7 @@ __device__ __forceinline__ void sample_row(const SampleParams& P, int row) {
       }
       by_list = false;
       by_value = sizeof(Raw) == 2;
+      crowd = true;
       if (by_value) continue;
     }
     draw_general(P, row, s, R, kmax);

@@ -1,5 +1,5 @@
 """vs_sample over the whole range of its settings: min-p of any size,
-and the uniform number 1."""
+the uniform number 1, and one answer for a row whatever the batch around it."""
 
 import pytest
 import torch
@@ -79,3 +79,68 @@ def test_the_number_one_takes_the_last_token(dtype, vocab, kw):
     x[4, :vocab] = x[4, :vocab] * 20
     u = torch.tensor([1.0, 1.0, 1.0, 1.0, 1.0]).cuda()
     check_both(x, u, vocab, t=0.25, **kw)
+
+
+# Rows of two tokens, 0 and v, whose first token's share 1 / (1 + exp(v / t)) lies within 6e-15 of the number u, with
+# v / t half way between two 64ths of an octave, where a mass by table and polynomial is off by up to 4e-14: (v, t, u).
+CLOSE = [(-0.3547404408454895, 1.981567144393921, 0.5446358919143677),
+         (-1.068514347076416, 0.744685173034668, 0.807656466960907),
+         (-1.775558352470398, 0.996565043926239, 0.8559039831161499),
+         (-2.5069146156311035, 0.8252211809158325, 0.9542559385299683),
+         (-0.4350297451019287, 1.3174697160720825, 0.5818082690238953),
+         (-0.7860302925109863, 0.5241159200668335, 0.8175336122512817),
+         (-0.22042067348957062, 0.6893056631088257, 0.5792686939239502),
+         (-0.17568178474903107, 0.5495159029960632, 0.5792518258094788),
+         (-0.2530349791049957, 0.5500776171684265, 0.6130138635635376)]
+
+
+@pytest.mark.parametrize("crowd", [False, True])
+@pytest.mark.parametrize("settings", [dict(k=2), dict(k=0), dict(k=2, p=1.0 - 2.0 ** -24), dict(k=2, m=1e-3)], ids=str)
+def test_one_answer_whatever_the_batch(settings, crowd):
+    """A row with a small top-k is listed in a small batch and goes another way
+    in a large one: the same masses, so the same token also where their last
+    units decide."""
+    n, vocab = len(CLOSE), 6000
+    v, t, u = (torch.tensor(a).cuda() for a in zip(*CLOSE))
+    x = torch.full((n, vocab), float("-inf"), device="cuda")
+    x[:, 17] = 0.0
+    x[:, 900] = v
+    kw = dict(k=0, p=1.0, m=0.0)
+    kw.update(settings)
+    if crowd:  # below the two tokens, out of the support
+        kw["m"] = max(kw["m"], 1e-3)
+        x[:, 1000:] = -50.0
+    few = vsb.sample(x, u, **{**tensors(n, 1.0, **kw), "temperature": t})
+    many = vsb.sample(x.repeat(4, 1), u.repeat(4), **{**tensors(4 * n, 1.0, **kw), "temperature": t.repeat(4)})
+    listed = vsb.sample(x.repeat(4, 1), u.repeat(4), temperature=t.repeat(4), top_k=kw["k"], top_p=kw["p"],
+                        min_p=kw["m"])
+    assert few["support_size"].eq(2).all()
+    for name in ("token", "support_size", "logprob"):
+        for other in (many, listed):
+            assert torch.equal(other[name].view(4, n).view(torch.int32),
+                               few[name].view(torch.int32)[None].expand(4, n)), name
+
+
+@pytest.mark.parametrize("top_k", [350, 512])
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_one_answer_for_crowded_rows(top_k, dtype):
+    """The cut falls among more equal tokens than a list holds, below values
+    that share the zeros' bin: taken by digits of the key in a small batch, from
+    the values' counts in a large one."""
+    vocab, n = 30_000, 32
+    g = torch.Generator().manual_seed(42)
+    x = torch.full((n, vocab), -1.0)
+    x[:, 100:400] = (torch.rand((n, 300), generator=g) * 2 - 1) * 2.0 ** -24
+    x[:, 150:200] = 0.0
+    x[:, 5] = 12.0
+    x[::2, 5] = 1e-3
+    x = x.to(dtype).cuda()
+    u = torch.rand(n, generator=g).cuda()
+    u[::4] = 1.0
+    for t in (1.0, 0.5):
+        many = vsb.sample(x, u, **tensors(n, t, top_k, 1.0, 0.0))
+        for r in range(0, n, 16):
+            few = vsb.sample(x[r:r + 16], u[r:r + 16], **tensors(16, t, top_k, 1.0, 0.0))
+            for name, w in few.items():
+                assert torch.equal(w.view(torch.int32), many[name][r:r + 16].view(torch.int32)), name
+        compare(many, x, u, vocab, *tensors(n, t, top_k, 1.0, 0.0).values())
