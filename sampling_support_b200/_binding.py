@@ -688,10 +688,11 @@ def _distill_args(logits, teacher_ids, teacher_logprob, temperature, tail, vocab
         raise ValueError("teacher_ids and teacher_logprob must be [rows, width]")
     width = shape[1]
     list_ld, unit = teacher_ids.stride()
-    if teacher_logprob.stride() != (list_ld, unit) or (unit != 1 and width > 1):
+    lp_ld, lp_unit = teacher_logprob.stride()
+    if rows <= 1 or width == 0:  # a stride that is never taken says nothing
+        list_ld = lp_ld = width
+    if lp_ld != list_ld or (width > 1 and (unit != 1 or lp_unit != 1)):
         raise ValueError("teacher_ids and teacher_logprob must have the same row stride, and unit stride in a row")
-    if rows <= 1 or width == 0:
-        list_ld = width
     t_at, t = _row_setting(temperature, "temperature", rows, torch.float32, dev)
     _cuda_device(logits)
     return DistillArgs(rows, vocab, ld, _dtype_code(logits), logits.data_ptr(), t_at, float(t),

@@ -232,3 +232,11 @@ def test_a_loss_near_zero(dtype, vocab):
         tol = 5e-6 * abs(qt - at) + 2.0 ** -23 * abs(mean) + 2.0 ** -24 * want + 1e-11
         assert want < 2e-3 and tol < 2e-7
         assert abs(float(out["loss"][r]) - want) <= tol, (r, float(out["loss"][r]), want, tol)
+
+
+def test_one_row_of_lists_of_different_widths():
+    x = logits_on("cuda", 1, 1003, F32, seed=13)
+    ids, lp = listed(2, 1003, 30, seed=39)
+    wide = torch.zeros((2, 50))
+    wide[:, :30] = lp
+    check(x, ids.cuda()[1:], wide.cuda()[1:, :30], 1.0, True, 1003)
