@@ -42,9 +42,9 @@ struct alignas(16) DistillCtx {
   float ref, lz;    // of the dense part: the whole row's, or what lies outside the list
   float coef;       // factor of the dense part: 1, or q_t - a_t
   float rall, lall; // the whole row's
-  // teacher: a_k = exp((lp_k - tref) - tlog).  In list mode tref is the list's largest value, so that values
-  // of any size keep their differences (one sum of both would round them away)
-  float tref, tlog;
+  // teacher: a_k = tnorm exp(lp_k - tref).  In list mode tref is the list's largest value, so that values of
+  // any size keep their differences (the logarithm of the sum added to it would round them away)
+  float tref, tnorm;
   uint32_t zero;    // no gradient (empty list, non-finite row)
   uint32_t dup;     // the list repeats an id
   uint32_t pad[5];
@@ -119,7 +119,7 @@ __device__ __forceinline__ void grad_pass(const Raw* __restrict__ row, G* __rest
     const int id = s < width ? ids[s] : -1;
     if (id >= j0 && id < j1 && (!k.dup || first_of(ids, s))) {
       const float q = ex2(fmaf(half_diff(value_of(row[id]), k.rall), c2, -k.lall));
-      float d = scale * (q - expf(lp[s] - k.tref - k.tlog));
+      float d = scale * (q - k.tnorm * expf(lp[s] - k.tref));
       if constexpr (ACC) d += old[i];
       out[id] = to_grad<G>(d);
     }
@@ -354,7 +354,7 @@ __global__ void __launch_bounds__(kDThreads) distill_fwd_kernel(DistillParams P)
   k.lz = outside ? static_cast<float>(log2(zr)) : k.lall;
   k.coef = tail ? (outside ? static_cast<float>(qt - at) : 0.f) : 1.f;
   k.tref = static_cast<float>(toff);
-  k.tlog = static_cast<float>(tlog);
+  k.tnorm = tail ? 1.f : static_cast<float>(1.0 / sum.a);
   k.zero = live ? 0u : 1u;
   k.dup = sh.dup;
   if (rank == 0 && tid == 0) {
@@ -668,7 +668,7 @@ __global__ void __launch_bounds__(kSThreads, 5) distill_stage_kernel(DistillPara
       k.lz = outside ? log2f(za) : k.lall;
       k.coef = tail ? (outside ? static_cast<float>(static_cast<double>(exp2f(half_diff(a, b) * c2) * za / zb) - sh.at) : 0.f) : 1.f;
       k.tref = sh.tref;
-      k.tlog = static_cast<float>(sh.tlog);
+      k.tnorm = tail ? 1.f : static_cast<float>(1.0 / sh.s0);
       k.zero = live ? 0u : 1u;
       k.dup = sh.dup;
       sh.k = k;
@@ -746,7 +746,8 @@ __global__ void __launch_bounds__(kSThreads, 5) distill_stage_kernel(DistillPara
       for (int s = tid; s < W; s += kSThreads) {
         const int id = ids[s];
         if (id >= j0 && id < j1)
-          out[id] = to_grad<G>(scale * (ex2(fmaf(half_diff(us[s], sh.k.rall), 2.f * sh.k.c, -sh.k.lall)) - expf(lps[s] - sh.k.tref - sh.k.tlog)));
+          out[id] = to_grad<G>(scale * (ex2(fmaf(half_diff(us[s], sh.k.rall), 2.f * sh.k.c, -sh.k.lall)) -
+                                        sh.k.tnorm * expf(lps[s] - sh.k.tref)));
       }
   }
 }
