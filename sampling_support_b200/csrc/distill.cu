@@ -11,14 +11,16 @@
 //               dl_j = (g / T) r_j (q_t - a_t)        else, r_j = q_j / q_t
 // (r_j on its own normaliser: q_j (1 - a_t / q_t) would divide by a q_t that
 // may be tiny.)  The elements outside L are summed apart from the list, so a
-// small q_t is a sum of its own and never a difference next to 1: each CTA
-// marks its row's list in a bitmap of one byte per eight elements, which costs
-// one shared load per 16-byte (bf16) vector of the pass.
+// small q_t is a sum of its own and never a difference next to 1.
 //
-// One cluster per row, one slice of the row per CTA: one pass for the
-// statistics; with a gradient requested in the same call a second one from
-// L2.  The backward kernel alone needs no exchange: (row, chunk) blocks read
-// the saved row constants.
+// Two forward kernels, one cluster per row and one slice of the row per CTA.
+// distill_stage_kernel copies its slice to shared memory, finds repeats with a
+// hash table and takes the listed elements out of the copy; all passes, the
+// gradient's too, run over that copy.  distill_fwd_kernel serves rows that eight
+// CTAs' shared memory does not hold (above 819,200 bf16 or 409,600 fp32
+// tokens): marks in a bitmap over the vocabulary, the row read from global
+// memory, a second pass from L2 for the gradient.  The backward kernel needs no
+// exchange: (row, chunk) blocks read the saved row constants.
 #include <algorithm>
 
 #include "common.cuh"
@@ -386,8 +388,8 @@ __global__ void __launch_bounds__(kDThreads) distill_fwd_kernel(DistillParams P)
 // memory of those that need them (the leader's, with a gradient everyone's).
 // A CTA holds its shared memory for a few microseconds of mostly latency, so
 // the rate is that of the slots: 40 KB slices, five CTAs per SM.  Measured: loss
-// and gradient of 2,048 x 151,936 bf16 in one call 259 us (4.8 TB/s of reads and
-// writes), the loss alone of 4,096 such rows 290 us (4.3 TB/s).
+// and gradient of 2,048 x 151,936 bf16 in one call 261 us (4.8 TB/s of reads and
+// writes), the loss alone of 4,096 such rows 291 us (4.3 TB/s).
 
 constexpr int kSThreads = 256;
 constexpr int kSWarps = kSThreads / 32;

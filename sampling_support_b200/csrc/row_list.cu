@@ -12,7 +12,7 @@
 //
 // Bound: a CTA holds its shared memory for several microseconds of mostly
 // latency (copy, floor, exchange, listing), so with 40 KB slices and five CTAs
-// per SM the rate is that of the slots: 187 us for k 64 of 2,048 x 151,936 bf16
+// per SM the rate is that of the slots: 191 us for k 64 of 2,048 x 151,936 bf16
 // (3.3 TB/s), 16.6 us for k 257 of 61 x 50,021 fp32, 8 us for a call of a few
 // rows, which is launch and latency.  No cluster barrier is waited for: the
 // floors and the first listed elements of every CTA are pushed, and a CTA

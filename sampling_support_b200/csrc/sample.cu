@@ -532,10 +532,10 @@ __device__ __forceinline__ void sample_row(const SampleParams& P, int row) {
 
 // One cluster per row, one CTA per SM.  Measured (device time): 128 x 151,936
 // bf16 with top-p 37 us, 512 with mixed filters 116 us (1.3 TB/s), 64 x 151,936 fp32 over
-// the whole vocabulary 64 us.  A bf16 row is bound by its one shared atomic per
+// the whole vocabulary 63 us.  A bf16 row is bound by its one shared atomic per
 // element and by the latency of what follows it (reduction, decision, the
 // token among its equals, about 12 us); an fp32 row by its masses pass (24 us
-// of the 64: the loads in flight that the registers allow, from L2).
+// of the 63: the loads in flight that the registers allow, from L2).
 // A list kernel before it may have its own share of the
 // rows; nothing after this kernel may start before that one is done.
 template <typename Raw>
@@ -564,9 +564,14 @@ static cudaError_t launch_rows(const Params& P, int clusters, int c, bool behind
 
 cudaError_t launch_sample(const SampleParams& Pin, vs_dtype dtype, cudaStream_t s) {
   SampleParams P = Pin;
-  // Whether all rows have a small top-k, or (per-row settings) some may.  In a larger batch of the
-  // latter kind the list kernel would hold up the other rows for a few microseconds, and the
-  // general kernel lists as well.
+  // Whether all rows have a small top-k, or (per-row settings) some may.  In the latter case the list
+  // kernel runs first up to 16 rows: the general kernel lists as well, at more latency, but does not
+  // hold up the rows without a top-k.  Device time in us, 151,936 bf16, list kernel first / general alone:
+  //   rows   all top-k 50   half top-k 50   no top-k
+  //      8   11.0 / 18.7    26.0 / 24.7     26.4 / 23.1
+  //     32   12.4 / 18.1    34.7 / 26.7     28.7 / 26.7
+  //    128   22.3 / 24.7    46.8 / 38.9     41.5 / 36.9
+  // so 8 us are won where all have one, 3 lost where none has; from 32 rows on it is 2 to 6 against 2 to 8.
   const bool all = (!P.top_k && sample_list_k(P.vocab, 1.f, P.top_k_scalar) > 0) ||
                    (!P.temperature && P.temperature_scalar == 0.f);
   if (all || ((P.top_k || P.temperature) && P.rows <= 16)) {
