@@ -144,3 +144,35 @@ def test_one_answer_for_crowded_rows(top_k, dtype):
             for name, w in few.items():
                 assert torch.equal(w.view(torch.int32), many[name][r:r + 16].view(torch.int32)), name
         compare(many, x, u, vocab, *tensors(n, t, top_k, 1.0, 0.0).values())
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_a_captured_call_whose_rows_change_kernels(dtype):
+    """Up to 16 rows with per-row settings take two kernels in one call, each
+    its share of the rows by their top-k: replayed after the settings change,
+    rows go from one to the other, and become greedy or refused."""
+    rows, vocab = 16, 20_011
+    x = logits_on("cuda", rows, vocab, dtype, seed=51)
+    u, kw = torch.full((rows,), 0.4, device="cuda"), tensors(rows, 0.8, 20, 0.9, 0.0)
+    vsb.sample(x, u, vocab=vocab, **kw)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        out = vsb.sample(x, u, vocab=vocab, **kw)
+    gen = torch.Generator().manual_seed(52)
+    for turn in range(4):
+        x.copy_(logits_on("cuda", rows, vocab, dtype, seed=60 + turn))
+        u.copy_(torch.rand(rows, generator=gen))
+        kw["top_k"].copy_(torch.randint(-1, 3, (rows,), generator=gen) * 300)  # off, 300 (listed), 600 (not)
+        kw["temperature"].copy_(torch.randint(0, 3, (rows,), generator=gen) * 0.5)
+        kw["min_p"].copy_(torch.randint(0, 2, (rows,), generator=gen) * 1e-3)
+        if turn == 3:
+            u[5] = 2.0
+        for _ in range(3):
+            g.replay()
+        torch.cuda.synchronize()
+        if turn == 3:
+            assert int(out["token"][5]) == -1 and int(out["status"][5]) == vsb.ROW_BAD_PARAM
+            keep = [r for r in range(rows) if r != 5]
+            compare({n: v[keep] for n, v in out.items()}, x[keep], u[keep], vocab, *(v[keep] for v in kw.values()))
+        else:
+            compare(out, x, u, vocab, *kw.values())
